@@ -16,13 +16,14 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgrpohead
 GH_OK, GH_ERR_INVALID_ARG, GH_ERR_UNSUPPORTED, GH_ERR_WORKSPACE, GH_ERR_CUDA = range(5)
 # device status bits
 GH_DEV_TARGET_OOR, GH_DEV_NONFINITE, GH_DEV_TIMEOUT, GH_DEV_NO_ACTIVE, GH_DEV_BAD_SEQ = 1, 2, 4, 8, 16
-DEV_BIT_NAMES = {1: "TARGET_OOR", 2: "NONFINITE", 4: "TIMEOUT", 8: "NO_ACTIVE", 16: "BAD_SEQ"}
+GH_DEV_BAD_ROW = 32
+DEV_BIT_NAMES = {1: "TARGET_OOR", 2: "NONFINITE", 4: "TIMEOUT", 8: "NO_ACTIVE", 16: "BAD_SEQ", 32: "BAD_ROW"}
 # dtypes / reductions
 GH_BF16, GH_FP32 = 0, 1
 GH_TOKEN_MEAN, GH_SEQ_MEAN, GH_FIXED = 0, 1, 2
 REDUCTIONS = {"token_mean": GH_TOKEN_MEAN, "seq_mean": GH_SEQ_MEAN, "fixed": GH_FIXED}
 RATIO_LEVELS = {"token": 0, "sequence": 1}
-NUM_KERNEL_KINDS = 18
+NUM_KERNEL_KINDS = 24
 NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024  # GH_NOALLOC_SCRATCH_BYTES
 
 
@@ -37,6 +38,15 @@ class GhGrpo(ctypes.Structure):
                 ("beta", c_float), ("delta", c_float), ("norm", c_double), ("ratio_level", c_int32),
                 ("reserved", c_int32), ("seq_policy", c_void_p), ("seq_kl", c_void_p), ("seq_count", c_void_p),
                 ("num_clipped", c_void_p)]
+
+
+class GhShaping(ctypes.Structure):
+    _fields_ = [("rows", c_int64), ("V", c_int64), ("tokens", c_void_p), ("num_tokens", c_int64),
+                ("hist_begin", c_void_p), ("hist_len", c_void_p), ("prompt_len", c_void_p), ("repetition", c_void_p),
+                ("presence", c_void_p), ("frequency", c_void_p), ("temperature", c_void_p),
+                ("bias_offsets", c_void_p), ("bias_tokens", c_void_p), ("bias_values", c_void_p),
+                ("bias_set", c_void_p), ("num_bias_sets", c_int32), ("num_bias", c_int32),
+                ("allow_bits", c_void_p), ("allow_row", c_void_p), ("num_allow", c_int32), ("reserved", c_int32)]
 
 
 # name -> (restype, argtypes)
@@ -72,6 +82,13 @@ SIGNATURES = {
     "grpo_dh_merge": (c_int32, [c_int32, c_int64, c_int64, c_int32, c_void_p, c_void_p, c_void_p, c_void_p]),
     "grpo_loss_from_sequence_totals": (c_int32, [c_int32, c_void_p, c_void_p, c_void_p, c_int32, c_double, c_float,
                                                  c_void_p, c_void_p, c_void_p]),
+    "grpo_shape_logits": (c_int32, [POINTER(GhShaping), c_void_p, c_int32, c_int64, c_void_p, c_int32, c_int64,
+                                    c_void_p, c_void_p]),
+    "grpo_shaped_logp_workspace_size": (c_size_t, [POINTER(GhShaping)]),
+    "grpo_shaped_logp": (c_int32, [POINTER(GhShaping), c_void_p, c_int32, c_int64, c_void_p, c_void_p, c_void_p,
+                                   c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "grpo_shaped_logp_backward": (c_int32, [POINTER(GhShaping), c_void_p, c_int32, c_int64, c_void_p, c_void_p,
+                                            c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_void_p]),
     "gh_status_string": (c_char_p, [c_int32]),
     "gh_last_error": (c_char_p, []),
     "gh_abi_version": (c_int32, []),

@@ -769,6 +769,153 @@ gh_status grpo_group_advantage(const float* rewards, int32_t num_seqs, int32_t g
   return GH_OK;
 }
 
+// ---------------------------------------------------------------- logit shaping
+static gh_status check_shaping(const gh_shaping* s) {
+  if (!s) return fail(GH_ERR_INVALID_ARG, "shaping is NULL");
+  if (s->rows < 0 || s->rows > (int64_t(1) << 30))
+    return fail(GH_ERR_INVALID_ARG, "rows=%lld out of range", (long long)s->rows);
+  if (s->V < 1 || s->V > (int64_t(1) << 28)) return fail(GH_ERR_INVALID_ARG, "V=%lld out of range", (long long)s->V);
+  // one CTA index counts (row, 1024-column segment) pairs at the finest
+  if (s->rows * shape_segments(s->V) > INT32_MAX)
+    return fail(GH_ERR_INVALID_ARG, "rows * ceil(V / 1024) = %lld is over 2^31 - 1: split the rows",
+                (long long)(s->rows * shape_segments(s->V)));
+  if (s->reserved != 0) return fail(GH_ERR_INVALID_ARG, "gh_shaping.reserved must be 0");
+  if (s->num_tokens < 0 || s->num_bias_sets < 0 || s->num_bias < 0 || s->num_allow < 0)
+    return fail(GH_ERR_INVALID_ARG, "num_tokens/num_bias_sets/num_bias/num_allow is negative");
+  if (s->hist_len && (!s->hist_begin || (s->num_tokens > 0 && !s->tokens)))
+    return fail(GH_ERR_INVALID_ARG, "hist_len is given, tokens or hist_begin is NULL");
+  if (s->bias_set && (!s->bias_offsets || (s->num_bias > 0 && (!s->bias_tokens || !s->bias_values))))
+    return fail(GH_ERR_INVALID_ARG, "bias_set is given, bias_offsets, bias_tokens or bias_values is NULL");
+  if (s->allow_row && s->num_allow > 0 && !s->allow_bits)
+    return fail(GH_ERR_INVALID_ARG, "allow_row is given, allow_bits is NULL");
+  return GH_OK;
+}
+
+static gh_status check_logits(const gh_shaping* s, const char* name, const void* p, int32_t dtype, int64_t ld) {
+  if (dtype != GH_BF16 && dtype != GH_FP32) return fail(GH_ERR_INVALID_ARG, "%s dtype=%d unknown", name, dtype);
+  if (s->rows == 0) return GH_OK;
+  if (!p) return fail(GH_ERR_INVALID_ARG, "%s is NULL", name);
+  if (ld < s->V || ld > (int64_t(1) << 32))
+    return fail(GH_ERR_INVALID_ARG, "%s row stride %lld is less than V=%lld or too large", name, (long long)ld,
+                (long long)s->V);
+  const uintptr_t elt = dtype == GH_BF16 ? 2 : 4;
+  if (reinterpret_cast<uintptr_t>(p) % elt != 0) return fail(GH_ERR_INVALID_ARG, "%s is not element-aligned", name);
+  return GH_OK;
+}
+
+// the output is the input itself (same element size and stride) or apart from it
+static bool same_or_apart(const gh_shaping* s, const void* in, int32_t dtype, int64_t ld, const void* out,
+                          int32_t out_dtype, int64_t out_ld) {
+  if (s->rows == 0 || (in == out && dtype == out_dtype && ld == out_ld)) return true;
+  const auto span = [&](int32_t dt, int64_t l) { return ((s->rows - 1) * l + s->V) * (dt == GH_BF16 ? 2 : 4); };
+  const uintptr_t a = reinterpret_cast<uintptr_t>(in), b = reinterpret_cast<uintptr_t>(out);
+  return a + static_cast<uintptr_t>(span(dtype, ld)) <= b || b + static_cast<uintptr_t>(span(out_dtype, out_ld)) <= a;
+}
+
+static ShapeArgs shape_args(const gh_shaping* s, const void* logits, int32_t dtype, int64_t ld, int32_t* status) {
+  ShapeArgs a{};
+  a.s = *s;
+  a.R = static_cast<int>(s->rows);
+  a.V = static_cast<int>(s->V);
+  a.dtype = a.out_dtype = dtype;
+  a.logits = logits;
+  a.ld = ld;
+  a.status = status;
+  return a;
+}
+
+gh_status grpo_shape_logits(const gh_shaping* shaping, const void* logits, int32_t dtype, int64_t ld, void* out,
+                            int32_t out_dtype, int64_t out_ld, int32_t* status, void* stream) {
+  g_last_error.clear();
+  gh_status r = check_shaping(shaping);
+  if (r != GH_OK) return r;
+  if (!status) return fail(GH_ERR_INVALID_ARG, "status is NULL");
+  if ((r = check_logits(shaping, "logits", logits, dtype, ld)) != GH_OK) return r;
+  if ((r = check_logits(shaping, "out", out, out_dtype, out_ld)) != GH_OK) return r;
+  if (!same_or_apart(shaping, logits, dtype, ld, out, out_dtype, out_ld))
+    return fail(GH_ERR_INVALID_ARG, "out overlaps logits (it may be logits itself, with the same dtype and stride)");
+  if (!device_is_sm103()) return fail(GH_ERR_UNSUPPORTED, "current device is not an sm_103 (GB300) GPU");
+  if (shaping->rows == 0) return GH_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  ShapeArgs a = shape_args(shaping, logits, dtype, ld, status);
+  a.out = out;
+  a.out_dtype = out_dtype;
+  a.out_ld = out_ld;
+  cudaError_t e = run(K_SHAPE, st, [&] { return launch_shape(a, st); });
+  if (e != cudaSuccess) return cuda_fail(e, "logit shaping launch");
+  return GH_OK;
+}
+
+static size_t shaped_zy_offset(const gh_shaping* s) {
+  return align_up(static_cast<size_t>(s->rows) * static_cast<size_t>(shape_segments(s->V)) * sizeof(float2), 256);
+}
+
+size_t grpo_shaped_logp_workspace_size(const gh_shaping* shaping) {
+  if (check_shaping(shaping) != GH_OK) return 0;
+  return shaped_zy_offset(shaping) + align_up(static_cast<size_t>(shaping->rows) * 4, 256);
+}
+
+gh_status grpo_shaped_logp(const gh_shaping* shaping, const void* logits, int32_t dtype, int64_t ld,
+                           const int32_t* targets, const uint8_t* mask, float* logp, float* lse, int32_t* status,
+                           void* ws, size_t ws_bytes, void* stream) {
+  g_last_error.clear();
+  gh_status r = check_shaping(shaping);
+  if (r != GH_OK) return r;
+  if (!status) return fail(GH_ERR_INVALID_ARG, "status is NULL");
+  if ((r = check_logits(shaping, "logits", logits, dtype, ld)) != GH_OK) return r;
+  if (shaping->rows > 0 && (!targets || !mask || !logp || !lse))
+    return fail(GH_ERR_INVALID_ARG, "targets/mask/logp/lse is NULL");
+  const size_t need = grpo_shaped_logp_workspace_size(shaping);
+  if (need > 0 && (!ws || ws_bytes < need))
+    return fail(GH_ERR_WORKSPACE, "shaped log-prob workspace needs %zu bytes, got %zu", need, ws ? ws_bytes : size_t(0));
+  if (need > 0 && !aligned16(ws)) return fail(GH_ERR_INVALID_ARG, "ws must be 16-byte aligned");
+  if (!device_is_sm103()) return fail(GH_ERR_UNSUPPORTED, "current device is not an sm_103 (GB300) GPU");
+  if (shaping->rows == 0) return GH_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  ShapeArgs a = shape_args(shaping, logits, dtype, ld, status);
+  a.targets = targets;
+  a.mask = mask;
+  a.part = static_cast<float2*>(ws);
+  a.zy = reinterpret_cast<float*>(static_cast<char*>(ws) + shaped_zy_offset(shaping));
+  a.logp = logp;
+  a.lse_out = lse;
+  cudaError_t e = run(K_SHAPED_LOGP, st, [&] { return launch_shaped_logp(a, st); });
+  if (e != cudaSuccess) return cuda_fail(e, "shaped log-prob launch");
+  e = run(K_SHAPED_MERGE, st, [&] { return launch_shaped_merge(a, st); });
+  if (e != cudaSuccess) return cuda_fail(e, "shaped log-prob merge launch");
+  return GH_OK;
+}
+
+gh_status grpo_shaped_logp_backward(const gh_shaping* shaping, const void* logits, int32_t dtype, int64_t ld,
+                                    const int32_t* targets, const uint8_t* mask, const float* lse, const float* coef,
+                                    const float* grad_out, void* dlogits, int64_t dlogits_ld, int32_t* status,
+                                    void* stream) {
+  g_last_error.clear();
+  gh_status r = check_shaping(shaping);
+  if (r != GH_OK) return r;
+  if (!status) return fail(GH_ERR_INVALID_ARG, "status is NULL");
+  if ((r = check_logits(shaping, "logits", logits, dtype, ld)) != GH_OK) return r;
+  if ((r = check_logits(shaping, "dlogits", dlogits, dtype, dlogits_ld)) != GH_OK) return r;
+  if (shaping->rows > 0 && (!targets || !mask || !lse || !coef))
+    return fail(GH_ERR_INVALID_ARG, "targets/mask/lse/coef is NULL");
+  if (!same_or_apart(shaping, logits, dtype, ld, dlogits, dtype, dlogits_ld))
+    return fail(GH_ERR_INVALID_ARG, "dlogits overlaps logits (it may be logits itself, with the same stride)");
+  if (!device_is_sm103()) return fail(GH_ERR_UNSUPPORTED, "current device is not an sm_103 (GB300) GPU");
+  if (shaping->rows == 0) return GH_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  ShapeArgs a = shape_args(shaping, logits, dtype, ld, status);
+  a.targets = targets;
+  a.mask = mask;
+  a.lse = lse;
+  a.coef = coef;
+  a.grad_out = grad_out;
+  a.out = dlogits;
+  a.out_ld = dlogits_ld;
+  cudaError_t e = run(K_SHAPED_GRAD, st, [&] { return launch_shaped_grad(a, st); });
+  if (e != cudaSuccess) return cuda_fail(e, "shaped log-prob gradient launch");
+  return GH_OK;
+}
+
 void gh_profile_enable(int32_t on) {
   std::lock_guard<std::mutex> lk(g_mu);
   g_prof.on = on != 0;
@@ -800,7 +947,8 @@ const char* gh_kernel_kind_name(int32_t kind) {
       "fwd_logits_lse_tc", "merge_lse", "grpo_loss", "gspo_segment", "dlogits_tc", "dh_gemm_tc",
       "dw_gemm_tc", "group_advantage", "fwd_logits_lse_f32", "dlogits_f32", "gemm_f32", "timeout_probe",
       "grpo_sequence_totals", "merge_lse_shards", "gspo_partials", "gspo_finish", "dh_merge",
-      "dhdw_gemm_tc"};
+      "dhdw_gemm_tc", "shape_logits", "shaped_logp", "shaped_logp_merge", "shaped_logp_grad", "adapter_low_rank",
+      "adapter_logits_tc"};
   if (kind < 0 || kind >= GH_NUM_KERNEL_KINDS) return "";
   return names[kind];
 }

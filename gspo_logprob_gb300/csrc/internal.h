@@ -45,6 +45,12 @@ enum KernelKind {
   K_GSPO_FINISH = 15,
   K_DH_MERGE = 16,
   K_DHDW_TC = 17,
+  K_SHAPE = 18,
+  K_SHAPED_LOGP = 19,
+  K_SHAPED_MERGE = 20,
+  K_SHAPED_GRAD = 21,
+  K_ADAPTER_LOW = 22,
+  K_ADAPTER_TC = 23,
 };
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -246,6 +252,37 @@ cudaError_t launch_advantage(const float* rewards, int num_seqs, int group_size,
 // dH = sum over shards (in shard order) of the fp32 partials [num_shards, n]
 cudaError_t launch_dh_merge(int num_shards, size_t n, bool to_bf16, const float* partials, void* out,
                             cudaStream_t st);
+// --- logit shaping (shape_kernels.cu) -----------------------------------------
+constexpr int SHAPE_MAX_HIST = (1 << 20) - 1;  // history tokens a row may have
+constexpr int SHAPE_MAX_BIAS = 2047;           // entries of a bias list
+struct ShapeArgs {
+  gh_shaping s;
+  int R, V;
+  int dtype, out_dtype;  // gh_dtype of the logits and of `out`
+  const void* logits;
+  int64_t ld;
+  void* out;  // shaped logits or dlogits
+  int64_t out_ld;
+  const int32_t* targets;
+  const uint8_t* mask;
+  const float* lse;
+  const float* coef;
+  const float* grad_out;
+  float2* part;  // [R, segments] (max, sum of exp(z' - max))
+  float* zy;     // [R]
+  float* logp;
+  float* lse_out;
+  int* status;
+  // set by the launchers
+  int cols, ntiles, rows_per_cta, nseg, table;
+  bool vec_in, vec_out;
+};
+int64_t shape_segments(int64_t V);
+cudaError_t launch_shape(ShapeArgs a, cudaStream_t st);
+cudaError_t launch_shaped_logp(ShapeArgs a, cudaStream_t st);   // segment partials and target logits
+cudaError_t launch_shaped_merge(ShapeArgs a, cudaStream_t st);  // logp and LSE from them
+cudaError_t launch_shaped_grad(ShapeArgs a, cudaStream_t st);
+
 cudaError_t launch_timeout_probe(int* status, uint64_t timeout_ns, cudaStream_t st);
 
 }  // namespace gh

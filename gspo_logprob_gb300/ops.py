@@ -18,7 +18,7 @@ from typing import Optional
 import torch
 
 from . import _abi
-from ._abi import GhGrpo, GhHead
+from ._abi import GhGrpo, GhHead, GhShaping
 
 _BF16 = torch.bfloat16
 _F32 = torch.float32
@@ -513,6 +513,191 @@ def grpo_group_advantage(rewards, group_size: int, eps: float = 1e-4, status: Op
                                        _stream(dev))
     _abi.check(code, "grpo_group_advantage")
     return adv
+
+
+# ------------------------------------------------------------------ logit shaping
+class Shaping:
+    """What ``make_shaping`` returns: the C struct and the tensors it points to
+    (kept alive by it, and free to be updated in place between calls)."""
+
+    def __init__(self, struct: GhShaping, tensors: dict, device):
+        self.struct = struct
+        self.tensors = tensors
+        self.device = device
+        self.ref = ctypes.byref(struct)
+        self.workspace_bytes = int(_lib().grpo_shaped_logp_workspace_size(self.ref))
+
+
+def make_shaping(rows: int, V: int, *, tokens=None, hist_begin=None, hist_len=None, prompt_len=None, repetition=None,
+                 presence=None, frequency=None, temperature=None, bias_offsets=None, bias_tokens=None,
+                 bias_values=None, bias_set=None, allow_bits=None, allow_row=None) -> Shaping:
+    """Describe how a batch's logits are shaped (gh_shaping in grpo_head.h).
+
+    Row i's history is ``tokens[hist_begin[i]:][:hist_len[i]]`` (int32 ids,
+    int64 begin, int32 length), its first ``prompt_len[i]`` tokens the prompt
+    (default 0).  ``repetition`` (> 0), ``presence``, ``frequency`` and
+    ``temperature`` (> 0) are fp32 [rows].  Row i's biases are entries
+    ``bias_offsets[k]:bias_offsets[k + 1]`` of ``bias_tokens`` (int32) and
+    ``bias_values`` (fp32), k = ``bias_set[i]`` (int32, -1: none); its allow mask
+    is row ``allow_row[i]`` (int32, -1: none) of ``allow_bits``, int32
+    [masks, ceil(V / 32)], bit j % 32 of word j // 32 set where token j is
+    allowed.  Everything left out is off.  The tensors are read by each call, so
+    a program keeps the result and updates them in place."""
+    R = int(rows)
+    dev = None
+    t = {}
+
+    def take(name, x, dtype, shape=None):
+        nonlocal dev
+        if x is None:
+            return None
+        _need(x, name, dtype, shape)
+        if dev is not None and x.device != dev:
+            raise ValueError(f"{name} is on {x.device}, the others on {dev}")
+        dev = x.device
+        t[name] = x
+        return x.data_ptr()
+
+    def together(a, name_a, others):
+        for name, x in others.items():
+            if (x is None) != (a is None):
+                raise ValueError(f"{name_a} and {name} go together")
+
+    together(hist_len, "hist_len", {"tokens": tokens, "hist_begin": hist_begin})
+    together(bias_set, "bias_set", {"bias_offsets": bias_offsets, "bias_tokens": bias_tokens,
+                                    "bias_values": bias_values})
+    together(allow_row, "allow_row", {"allow_bits": allow_bits})
+    if prompt_len is not None and hist_len is None:
+        raise ValueError("prompt_len needs hist_len")
+    s = GhShaping(rows=R, V=int(V))
+    s.tokens = take("tokens", tokens, torch.int32)
+    s.num_tokens = tokens.numel() if tokens is not None else 0
+    s.hist_begin = take("hist_begin", hist_begin, torch.int64, (R,))
+    s.hist_len = take("hist_len", hist_len, torch.int32, (R,))
+    s.prompt_len = take("prompt_len", prompt_len, torch.int32, (R,))
+    s.repetition = take("repetition", repetition, _F32, (R,))
+    s.presence = take("presence", presence, _F32, (R,))
+    s.frequency = take("frequency", frequency, _F32, (R,))
+    s.temperature = take("temperature", temperature, _F32, (R,))
+    if bias_set is not None:
+        if bias_offsets.dim() != 1 or bias_offsets.numel() < 1:
+            raise ValueError("bias_offsets must be [lists + 1]")
+        s.bias_offsets = take("bias_offsets", bias_offsets, torch.int32)
+        s.bias_tokens = take("bias_tokens", bias_tokens, torch.int32)
+        s.bias_values = take("bias_values", bias_values, _F32, (bias_tokens.numel(),))
+        s.bias_set = take("bias_set", bias_set, torch.int32, (R,))
+        s.num_bias_sets = bias_offsets.numel() - 1
+        s.num_bias = bias_tokens.numel()
+    if allow_row is not None:
+        words = (int(V) + 31) // 32
+        if allow_bits.dim() != 2 or allow_bits.shape[1] != words:
+            raise ValueError(f"allow_bits must be [masks, {words}], got {tuple(allow_bits.shape)}")
+        s.allow_bits = take("allow_bits", allow_bits, torch.int32)
+        s.allow_row = take("allow_row", allow_row, torch.int32, (R,))
+        s.num_allow = allow_bits.shape[0]
+    return Shaping(s, t, dev)
+
+
+def _gh_dtype(t: torch.dtype, name: str) -> int:
+    if t == _BF16:
+        return _abi.GH_BF16
+    if t == _F32:
+        return _abi.GH_FP32
+    raise TypeError(f"{name} must be bfloat16 or float32, got {t}")
+
+
+def _need_logits(t: torch.Tensor, name: str, shaping: Shaping, dtype=None):
+    """Row-strided [rows, V] logits: any row stride, contiguous columns.  Returns (gh_dtype, row stride)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if shaping.device is not None and t.device != shaping.device:
+        raise ValueError(f"{name} is on {t.device}, the shaping on {shaping.device}")
+    s = shaping.struct
+    if tuple(t.shape) != (s.rows, s.V):
+        raise ValueError(f"{name} must have shape {(s.rows, s.V)}, got {tuple(t.shape)}")
+    if s.V > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    ld = t.stride(0) if s.rows > 1 else max(s.V, 1)
+    if ld < s.V:
+        raise ValueError(f"{name} has rows that overlap")
+    return _gh_dtype(t.dtype, name), ld
+
+
+@_nvtx
+def grpo_shape_logits(logits, shaping: Shaping, *, out=None, out_dtype=None, status: Optional[torch.Tensor] = None):
+    """Shaped logits z' [rows, V] of ``logits`` (bf16 or fp32, any row stride),
+    in ``out`` (which may be ``logits`` itself) or a new tensor of ``out_dtype``
+    (default: the logits' type).  Returns a dict with logits and status."""
+    dt, ld = _need_logits(logits, "logits", shaping)
+    if out is None:
+        out = torch.empty(logits.shape, dtype=out_dtype or logits.dtype, device=logits.device)
+    odt, old = _need_logits(out, "out", shaping, out_dtype)
+    dev = logits.device
+    st = new_status(dev) if status is None else status
+    code = _lib().grpo_shape_logits(shaping.ref, logits.data_ptr(), dt, ld, out.data_ptr(), odt, old, st.data_ptr(),
+                                    _stream(dev))
+    _abi.check(code, "grpo_shape_logits")
+    return dict(logits=out, status=st)
+
+
+@_nvtx
+def grpo_shaped_logp(logits, targets, mask, shaping: Shaping, *, out: Optional[dict] = None,
+                     status: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """Selected-token log-prob and LSE [rows] fp32 under the shaped logits (which
+    are never written); rows with mask 0 are not read and give 0.  ``out`` may
+    hold preallocated logp and lse; ``workspace`` as in grpo_head_forward
+    (``shaping.workspace_bytes`` bytes).  Returns a dict with logp, lse, status."""
+    dt, ld = _need_logits(logits, "logits", shaping)
+    R = shaping.struct.rows
+    _need(targets, "targets", torch.int32, (R,))
+    _need(mask, "mask", torch.uint8, (R,))
+    dev = logits.device
+    out = {} if out is None else out
+    logp = _need(out["logp"], "logp", _F32, (R,)) if out.get("logp") is not None else \
+        torch.empty(R, dtype=_F32, device=dev)
+    lse = _need(out["lse"], "lse", _F32, (R,)) if out.get("lse") is not None else \
+        torch.empty(R, dtype=_F32, device=dev)
+    st = new_status(dev) if status is None else status
+    nbytes = shaping.workspace_bytes
+    ws = _caller_workspace(workspace, nbytes) if workspace is not None else WORKSPACE.get(dev, nbytes)
+    code = _lib().grpo_shaped_logp(shaping.ref, logits.data_ptr(), dt, ld, targets.data_ptr(), mask.data_ptr(),
+                                   logp.data_ptr(), lse.data_ptr(), st.data_ptr(), ws.data_ptr(), nbytes,
+                                   _stream(dev))
+    _abi.check(code, "grpo_shaped_logp")
+    out.update(logp=logp, lse=lse, status=st)
+    return out
+
+
+@_nvtx
+def grpo_shaped_logp_backward(logits, targets, mask, shaping: Shaping, lse, coef, *, grad_out=None, dlogits=None,
+                              status: Optional[torch.Tensor] = None):
+    """Gradient with respect to the raw logits, [rows, V] in their type, from each
+    row's LSE (of grpo_shaped_logp) and coef = d loss / d logp; rows with mask 0
+    or coef 0 are not read and get zeros.  ``dlogits`` may be ``logits`` itself.
+    Returns a dict with dlogits and status."""
+    dt, ld = _need_logits(logits, "logits", shaping)
+    R = shaping.struct.rows
+    _need(targets, "targets", torch.int32, (R,))
+    _need(mask, "mask", torch.uint8, (R,))
+    _need(lse, "lse", _F32, (R,))
+    _need(coef, "coef", _F32, (R,))
+    if grad_out is not None:
+        _need(grad_out, "grad_out", _F32)
+    dev = logits.device
+    if dlogits is None:
+        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+    _, dld = _need_logits(dlogits, "dlogits", shaping, logits.dtype)
+    st = new_status(dev) if status is None else status
+    code = _lib().grpo_shaped_logp_backward(shaping.ref, logits.data_ptr(), dt, ld, targets.data_ptr(),
+                                            mask.data_ptr(), lse.data_ptr(), coef.data_ptr(),
+                                            None if grad_out is None else grad_out.data_ptr(), dlogits.data_ptr(), dld,
+                                            st.data_ptr(), _stream(dev))
+    _abi.check(code, "grpo_shaped_logp_backward")
+    return dict(dlogits=dlogits, status=st)
 
 
 def timeout_probe(timeout_ns: int, dev=None):

@@ -72,7 +72,10 @@ enum {
   GH_DEV_NONFINITE = 2,   /* a non-finite LSE/logp/loss term was produced              */
   GH_DEV_TIMEOUT = 4,     /* a bounded pipeline wait gave up; outputs are incomplete   */
   GH_DEV_NO_ACTIVE = 8,   /* token/sequence mean with no active token: loss 0, coef 0  */
-  GH_DEV_BAD_SEQ = 16     /* seq_id/seg_id out of range or not laid out as documented  */
+  GH_DEV_BAD_SEQ = 16,    /* seq_id/seg_id out of range or not laid out as documented  */
+  GH_DEV_BAD_ROW = 32     /* a row's history, bias list, allow mask or adapter lies outside
+                             its array, or its temperature or repetition penalty is not a
+                             positive finite number; the row is computed without it        */
 };
 
 typedef enum { GH_BF16 = 0, GH_FP32 = 1 } gh_dtype;
@@ -371,6 +374,94 @@ gh_status grpo_group_advantage(const float* rewards, int32_t num_seqs, int32_t g
 gh_status grpo_head_forward_noalloc(const gh_head* head, const gh_grpo* grpo, float* logp, float* lse,
                                     float* coef, float* loss3, int32_t* status, void* stream);
 
+/*
+ * How the logits of a batch are shaped before they are a distribution, as
+ * samplers do: penalties for repeated tokens, biases, allow (grammar) masks and
+ * a temperature, each per row.  With h the row's history (its first prompt_len
+ * tokens the prompt, the others the output) and c_j the times j occurs in the
+ * output part:
+ *   z1 = z / repetition if z > 0 else z * repetition   (j anywhere in h)
+ *   z2 = z1 - frequency c_j - presence [c_j > 0] + bias_j
+ *   z' = z2 / temperature, -inf where the row's allow mask has a 0 bit.
+ * Every array is on the device and may be updated in place between calls (a
+ * program appends its new tokens and raises hist_len); the library reads it on
+ * the stream of each call.  Any feature whose pointer is NULL is off.
+ *
+ * Histories: row i's is tokens[hist_begin[i] .. + hist_len[i]); at most 2^20 - 1
+ * tokens each; rows may share tokens.  Consecutive rows whose histories are
+ * prefixes of one another (a training sequence) are the fast case of the
+ * log-prob and its gradient.  Ids outside [0, V) in a history or a bias list
+ * have no effect.  The last entry of a token in a bias list counts.
+ *
+ * What lies outside its array, or is no valid factor, sets GH_DEV_BAD_ROW and
+ * the row is computed without it.
+ */
+typedef struct {
+  int64_t rows;                /* rows of the logits                                        */
+  int64_t V;                   /* vocabulary size                                           */
+  const int32_t* tokens;       /* [num_tokens] the histories' token ids                     */
+  int64_t num_tokens;
+  const int64_t* hist_begin;   /* [rows] first token of each row's history                  */
+  const int32_t* hist_len;     /* [rows] its length; NULL: no histories                     */
+  const int32_t* prompt_len;   /* [rows] tokens of it that are the prompt's; NULL: 0        */
+  const float* repetition;     /* [rows] > 0; 1 = off                                       */
+  const float* presence;       /* [rows]                                                    */
+  const float* frequency;      /* [rows]                                                    */
+  const float* temperature;    /* [rows] > 0                                                */
+  const int32_t* bias_offsets; /* [num_bias_sets + 1] bounds of each bias list              */
+  const int32_t* bias_tokens;  /* [num_bias]                                                */
+  const float* bias_values;    /* [num_bias]                                                */
+  const int32_t* bias_set;     /* [rows] the row's list, -1: none; NULL: no biases          */
+  int32_t num_bias_sets;
+  int32_t num_bias;            /* entries of all lists; at most 2047 in one list            */
+  const uint32_t* allow_bits;  /* [num_allow, ceil(V / 32)]; bit j % 32 of word j / 32: 1 =
+                                  token j is allowed                                        */
+  const int32_t* allow_row;    /* [rows] the row's mask, -1: none; NULL: no masks           */
+  int32_t num_allow;
+  int32_t reserved;            /* must be 0                                                 */
+} gh_shaping;
+
+/*
+ * Shaped logits: out [rows, V] = z' of logits [rows, V].  dtype and out_dtype
+ * are gh_dtype; ld and out_ld the row strides in elements (>= V).  Any stride
+ * and element-aligned pointer is taken; rows that start on 16-byte boundaries
+ * are the fast case.  out may be logits itself with the same dtype and stride,
+ * and may not overlap it otherwise.  A bf16 output is rounded once, from fp32.
+ * Logits in barred places may hold anything (NaN too); they are not read.
+ */
+gh_status grpo_shape_logits(const gh_shaping* shaping, const void* logits, int32_t dtype, int64_t ld, void* out,
+                            int32_t out_dtype, int64_t out_ld, int32_t* status, void* stream);
+
+/* Bytes of scratch `ws` grpo_shaped_logp needs (0 for invalid arguments). */
+size_t grpo_shaped_logp_workspace_size(const gh_shaping* shaping);
+/*
+ * Selected-token log-prob and LSE under the shaped logits, which are never
+ * written: logp_i = z'_{i,y_i} - LSE_i, in one pass over the logits.  Outputs
+ * [rows] fp32.  mask (as in gh_head) is authoritative: rows with mask 0 are not
+ * read and get logp = lse = 0.  For active rows: logp is NaN and
+ * GH_DEV_TARGET_OOR set for a target outside [0, V); -inf for a barred target;
+ * logp = lse = -inf where the mask leaves nothing; GH_DEV_NONFINITE is set for
+ * each of the last two.  The results are bitwise independent of the other rows
+ * and of the row strides.
+ */
+gh_status grpo_shaped_logp(const gh_shaping* shaping, const void* logits, int32_t dtype, int64_t ld,
+                           const int32_t* targets, const uint8_t* mask, float* logp, float* lse, int32_t* status,
+                           void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Gradient of the shaped log-prob with respect to the raw logits, given each
+ * row's LSE (from grpo_shaped_logp) and coef = d loss / d logp:
+ *   dz_j = g coef_i (1[j = y_i] - exp(z'_j - LSE_i)) dz'_j/dz_j,
+ *   dz'/dz = (repetition, its inverse or 1) / temperature, 0 where barred
+ * (g = *grad_out, or 1 if NULL), in the logits' dtype.  Rows with mask 0,
+ * coef 0 or LSE -inf get zeros and are not read.  dlogits may be logits itself
+ * (same stride), and may not overlap it otherwise.
+ */
+gh_status grpo_shaped_logp_backward(const gh_shaping* shaping, const void* logits, int32_t dtype, int64_t ld,
+                                    const int32_t* targets, const uint8_t* mask, const float* lse, const float* coef,
+                                    const float* grad_out, void* dlogits, int64_t dlogits_ld, int32_t* status,
+                                    void* stream);
+
 /* Human-readable name of a gh_status. */
 const char* gh_status_string(gh_status s);
 /* Message of the last error returned on the calling thread ("" if none). */
@@ -391,9 +482,11 @@ int32_t gh_abi_version(void);
  * 5 dH GEMM, 6 dW GEMM, 7 advantage, 8 fp32 forward, 9 fp32 dlogits,
  * 10 fp32 GEMM, 11 timeout probe, 12 GRPO loss from sequence totals, 13 shard merge,
  * 14 GSPO partials, 15 GSPO loss from partials, 16 dH shard merge, 17 dH and dW
- * GEMMs of a vocabulary block in one launch.
+ * GEMMs of a vocabulary block in one launch, 18 logit shaping, 19 shaped
+ * log-prob, 20 its merge, 21 its gradient, 22 adapters' low-rank activations,
+ * 23 head product with adapters.
  */
-#define GH_NUM_KERNEL_KINDS 18
+#define GH_NUM_KERNEL_KINDS 24
 void gh_profile_enable(int32_t on);
 void gh_profile_reset(void);
 gh_status gh_profile_read(int32_t kind, int64_t* launches, double* total_ms);

@@ -1,0 +1,149 @@
+"""fp64 oracle of logit shaping: penalties, biases, allow masks, temperature;
+the selected log-prob under the shaped logits and its gradient.
+
+Plain NumPy, one row at a time, with dictionaries for the counts.  Test
+infrastructure only; shares nothing with the CUDA path.  Pinned by closed
+forms and central differences in tests/test_oracle_shaping.py.
+"""
+from __future__ import annotations
+
+import numpy as np
+
+MAX_HIST = (1 << 20) - 1
+MAX_BIAS = 2047
+
+
+def _factor(x):
+    return (float(x), False) if np.isfinite(x) and x > 0 else (1.0, True)
+
+
+def shape_row(z, history=(), prompt_len=0, repetition=1.0, presence=0.0, frequency=0.0, bias=(), allowed=None,
+              temperature=1.0):
+    """(z', dz'/dz, magnitude) of one row.  ``bias``: (token, value) pairs, the
+    last of a token counts; ``allowed``: a boolean per token or None.
+    ``magnitude`` bounds the terms that make up z' (for rounding bounds)."""
+    z = np.asarray(z, dtype=np.float64)
+    V = z.size
+    out = z.copy()
+    slope = np.ones(V)
+    theta, _ = _factor(repetition)
+    T, _ = _factor(temperature)
+    plen = min(max(int(prompt_len), 0), len(history))
+    counts, seen = {}, set()
+    for k, j in enumerate(history):
+        if 0 <= j < V:
+            seen.add(int(j))
+            if k >= plen:
+                counts[int(j)] = counts.get(int(j), 0) + 1
+    for j in seen:
+        slope[j] = 1.0 / theta if z[j] > 0 else theta
+        out[j] = z[j] * slope[j]
+    mag = np.abs(out)
+    for j, c in counts.items():
+        out[j] -= frequency * c + presence
+        mag[j] += abs(frequency * c) + abs(presence)
+    for j, b in {int(j): float(b) for j, b in bias}.items():
+        if 0 <= j < V:
+            out[j] += b
+            mag[j] += abs(b)
+    out, slope, mag = out / T, slope / T, mag / T
+    if allowed is not None:
+        out = np.where(allowed, out, -np.inf)
+        slope = np.where(allowed, slope, 0.0)
+        mag = np.where(allowed, mag, 0.0)
+    return out, slope, mag
+
+
+def row_inputs(batch, i, V):
+    """Keyword arguments of ``shape_row`` for row i of a batch of arrays (names
+    as in make_shaping), and whether something of the row was left out."""
+    kw, bad = {}, False
+    for name in ("repetition", "temperature"):
+        if batch.get(name) is not None:
+            kw[name], b = _factor(batch[name][i])
+            bad |= b
+    for name in ("presence", "frequency"):
+        if batch.get(name) is not None:
+            kw[name] = float(batch[name][i])
+    off = kw.get("repetition", 1.0) == 1.0 and kw.get("presence", 0.0) == 0.0 and kw.get("frequency", 0.0) == 0.0
+    if batch.get("hist_len") is not None and not off:
+        b, n = int(batch["hist_begin"][i]), int(batch["hist_len"][i])
+        if b < 0 or n < 0 or n > MAX_HIST or b + n > len(batch["tokens"]):
+            bad = True
+        else:
+            kw["history"] = [int(x) for x in batch["tokens"][b:b + n]]
+            kw["prompt_len"] = int(batch["prompt_len"][i]) if batch.get("prompt_len") is not None else 0
+    if batch.get("bias_set") is not None:
+        k = int(batch["bias_set"][i])
+        if k < -1 or k >= len(batch["bias_offsets"]) - 1:
+            bad = True
+        elif k >= 0:
+            b, e = int(batch["bias_offsets"][k]), int(batch["bias_offsets"][k + 1])
+            if b < 0 or e < b or e > len(batch["bias_tokens"]) or e - b > MAX_BIAS:
+                bad = True
+            else:
+                kw["bias"] = list(zip(batch["bias_tokens"][b:e], batch["bias_values"][b:e]))
+    if batch.get("allow_row") is not None:
+        k = int(batch["allow_row"][i])
+        if k < -1 or k >= len(batch["allow_bits"]):
+            bad = True
+        elif k >= 0:
+            words = np.asarray(batch["allow_bits"][k]).view(np.uint32)
+            kw["allowed"] = np.array([(int(words[j // 32]) >> (j % 32)) & 1 for j in range(V)], dtype=bool)
+    return kw, bad
+
+
+def shape_logits(Z, batch):
+    """(z', dz'/dz, magnitude) [rows, V] and the rows where something was left out."""
+    Z = np.asarray(Z, dtype=np.float64)
+    res = [np.empty_like(Z) for _ in range(3)]
+    bad = np.zeros(Z.shape[0], dtype=bool)
+    for i in range(Z.shape[0]):
+        kw, bad[i] = row_inputs(batch, i, Z.shape[1])
+        for dst, src in zip(res, shape_row(Z[i], **kw)):
+            dst[i] = src
+    return res[0], res[1], res[2], bad
+
+
+def row_lse(z):
+    """log sum exp of one row; -inf where nothing is left."""
+    top = np.max(z)
+    if top == -np.inf:
+        return -np.inf
+    return float(top + np.log(np.sum(np.exp(z - top))))
+
+
+def shaped_logp(Zp, targets, mask):
+    """(logp, lse) of shaped rows: 0 for inactive ones, NaN for a target out of
+    range, -inf for a barred target."""
+    n, V = Zp.shape
+    logp, lse = np.zeros(n), np.zeros(n)
+    for i in range(n):
+        if not mask[i]:
+            continue
+        lse[i] = row_lse(Zp[i])
+        y = int(targets[i])
+        if not 0 <= y < V:
+            logp[i] = np.nan
+        elif Zp[i, y] == -np.inf:
+            logp[i] = -np.inf
+        else:
+            top = np.max(Zp[i])
+            logp[i] = (Zp[i, y] - top) - np.log(np.sum(np.exp(Zp[i] - top)))
+    return logp, lse
+
+
+def shaped_logp_grad(Zp, slope, targets, mask, lse, coef, grad_out=1.0):
+    """d (sum_i coef_i logp_i) / dz times grad_out."""
+    n, V = Zp.shape
+    G = np.zeros((n, V))
+    for i in range(n):
+        if not mask[i] or coef[i] == 0 or lse[i] == -np.inf:
+            continue
+        p = np.exp(Zp[i] - lse[i])
+        d = -p
+        y = int(targets[i])
+        if 0 <= y < V:
+            d[y] += 1.0
+        G[i] = np.where(slope[i] > 0, grad_out * coef[i] * d * slope[i], 0.0)
+    return G
