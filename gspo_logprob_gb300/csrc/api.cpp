@@ -775,9 +775,9 @@ static gh_status check_shaping(const gh_shaping* s) {
   if (s->rows < 0 || s->rows > (int64_t(1) << 30))
     return fail(GH_ERR_INVALID_ARG, "rows=%lld out of range", (long long)s->rows);
   if (s->V < 1 || s->V > (int64_t(1) << 28)) return fail(GH_ERR_INVALID_ARG, "V=%lld out of range", (long long)s->V);
-  // one CTA index counts (row, 1024-column segment) pairs at the finest
+  // one CTA index counts (row, segment) pairs at the finest
   if (s->rows * shape_segments(s->V) > INT32_MAX)
-    return fail(GH_ERR_INVALID_ARG, "rows * ceil(V / 1024) = %lld is over 2^31 - 1: split the rows",
+    return fail(GH_ERR_INVALID_ARG, "rows * ceil(V / 512) = %lld is over 2^31 - 1: split the rows",
                 (long long)(s->rows * shape_segments(s->V)));
   if (s->reserved != 0) return fail(GH_ERR_INVALID_ARG, "gh_shaping.reserved must be 0");
   if (s->num_tokens < 0 || s->num_bias_sets < 0 || s->num_bias < 0 || s->num_allow < 0)

@@ -255,6 +255,7 @@ cudaError_t launch_dh_merge(int num_shards, size_t n, bool to_bf16, const float*
 // --- logit shaping (shape_kernels.cu) -----------------------------------------
 constexpr int SHAPE_MAX_HIST = (1 << 20) - 1;  // history tokens a row may have
 constexpr int SHAPE_MAX_BIAS = 2047;           // entries of a bias list
+constexpr int SHAPE_MIN_SEG = 512;             // columns of the shortest partial of the log-prob
 struct ShapeArgs {
   gh_shaping s;
   int R, V;
@@ -274,7 +275,7 @@ struct ShapeArgs {
   float* lse_out;
   int* status;
   // set by the launchers
-  int cols, ntiles, rows_per_cta, nseg, table;
+  int cols, ntiles, rows_per_cta, nseg;
   bool vec_in, vec_out;
 };
 int64_t shape_segments(int64_t V);

@@ -10,17 +10,32 @@
 //   logp = z'_y - LSE(z'),  d logp / d z_j = ([j = y] - p_j) d z'_j / d z_j.
 //
 // One kernel serves the three calls.  A CTA owns a range of columns for a block
-// of rows and keeps the counts of its columns in shared memory: one word per
-// column (output count, prompt flag, bias entry) and one bit per column that
-// says whether the word is in use, so that eight untouched columns cost one
-// byte load.  Rows whose history is that of the row before plus some tokens
-// (consecutive rows of a training sequence) only add those tokens; other rows
-// rebuild the words by a scan of their history.
+// of rows.  What a row's history and bias list say about its tokens is kept in
+// shared memory as a ranked set: a bit per column that is in the set, the set's
+// size before each 32 columns, and one word per member (output count, prompt
+// flag, bias entry) at its rank.  That is 6 bytes per 32 columns and 4 per
+// distinct token, against 4 bytes per column for a table of words, so a CTA can
+// take a fifth of a 151936-column row and a history is scanned 5 times, not 10.
 //
-// Columns are cut into segments of 1024, each the work of one warp: 4 chunks of
-// 256 columns, lane l holding columns 8l..8l+7 of a chunk.  The log-prob keeps
-// one (max, sum) per row and segment, so its bits depend on V alone: not on the
-// columns per CTA, the rows per CTA or the other rows of the batch.
+// Rows whose history is that of the row before plus some tokens (consecutive
+// rows of a training sequence) form a chain: the set is built once, from the
+// chain's last row, and each row only adds its new tokens to the words.  A warp
+// owns the columns of its segments for all of the chain, so it adds the tokens
+// that fall there itself and the warps need no barrier between rows.
+//
+// Columns are cut into segments of 4 (bf16; fp32: 2) chunks of 256 columns, 2 KB
+// of a row.  A warp stages its segments in shared memory by asynchronous copies,
+// one ahead of the one it works on (64 KB in flight per SM, which covers the
+// latency of HBM at its rate); it reads the allow bits one segment earlier still,
+// so that barred logits are not copied.  Rows that do not start on a 16-byte
+// boundary are copied from the boundary before and shifted by words as they are
+// read back.  A segment has a sparse pass over the members, a lane per 32
+// columns, and a dense pass, lane l taking columns 8l..8l+7 of a chunk.  The
+// log-prob's sparse pass puts -inf in the members' staged places, so that the
+// dense pass knows nothing of them; shaped logits and gradients are overwritten
+// at the members after the dense pass.  The log-prob keeps one (max, sum) per row
+// and segment, so its bits depend on V and the type alone: not on the columns or
+// rows per CTA, the strides or the other rows of the batch.
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -31,13 +46,25 @@ namespace {
 
 constexpr int SH_THREADS = 256;
 constexpr int SH_WARPS = SH_THREADS / 32;
-constexpr int SH_CHUNKS = 4;                     // 16-byte loads a lane has in flight
-constexpr int SH_SEG = SH_CHUNKS * 256;          // columns per warp segment
-constexpr int SH_MAX_COLS = 16384;               // columns per CTA: 64 KB of words, three CTAs per SM
+constexpr int SH_CTAS = 4;                       // resident per SM: 32 warps of 64 registers a thread
+constexpr int SH_MAX_COLS = 32768;               // columns per CTA
+constexpr int SH_SET = 2048;                     // members the words have room for
 constexpr int SH_MAX_ROWS = 32;                  // rows per CTA (one lane each in the set-up)
 constexpr float SH_LOG2E = 1.4426950408889634f;
+constexpr float SH_LOWEST = 3.402823466e38f;     // the largest finite fp32
+constexpr float SH_BIG = 1e37f;                  // beyond this a step to base 2 may overflow
+static_assert(SH_SET % SHAPE_MIN_SEG == 0, "a range of SH_SET columns, which always fits, is whole segments");
 
-// the word of a column: bits 0-19 output count, 20 seen in the prompt, 21-31
+template <class T>
+struct ShSeg {
+  static constexpr int CHUNKS = sizeof(T) == 2 ? 4 : 2;  // 16 registers of raw logits a lane
+  static constexpr int COLS = CHUNKS * 256;
+  static constexpr int WORDS = COLS / 32;                // lanes of the sparse pass
+  static constexpr int LANE16 = static_cast<int>(sizeof(T)) / 2;  // 16-byte words of a lane's eight columns
+  static constexpr uint32_t FULL = sizeof(T) == 2 ? 0xffffffffu : 0xffffu;  // a byte of columns per chunk
+};
+
+// the word of a member: bits 0-19 output count, 20 seen in the prompt, 21-31
 // bias entry + 1 of the row's list
 constexpr uint32_t SH_COUNT = SHAPE_MAX_HIST;
 constexpr uint32_t SH_PROMPT = 1u << 20;
@@ -46,8 +73,9 @@ static_assert(SH_COUNT + 1 == SH_PROMPT && SHAPE_MAX_BIAS == (1 << (32 - SH_BIAS
 
 enum { SHAPE_OUT = 0, SHAPE_LOGP = 1, SHAPE_GRAD = 2 };
 
-// how the words go from the row before to this one
-enum { TAB_NONE = 0, TAB_KEEP = 1, TAB_ADD1 = 2, TAB_ADD = 3, TAB_BUILD = 4 };  // NONE: the row uses no words
+// how a row's set follows from the row before: none needed, the same, one more
+// output token, more tokens, built anew
+enum { TAB_NONE = 0, TAB_KEEP = 1, TAB_ADD1 = 2, TAB_ADD = 3, TAB_BUILD = 4 };
 
 struct ShRow {
   long long begin;  // first history token
@@ -56,10 +84,10 @@ struct ShRow {
   int allow;        // row of allow_bits or -1
   int y;
   int tab;          // TAB_*
-  int add_from;     // TAB_ADD: history tokens [add_from, len) are new; TAB_ADD1: the token itself
+  int add;          // TAB_ADD: history tokens [add, len) are new; TAB_ADD1: the token itself
   float rep, inv_rep, pres, freq;
   float inv_t;
-  float scale;      // GRAD: grad_out * coef
+  float scale;      // GRAD: grad_out * coef / T
   float lse;        // GRAD
 };
 
@@ -77,49 +105,136 @@ __device__ __forceinline__ float sh_from_float<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 sh_from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
-// eight consecutive elements from p; `n` of them exist, `vec`: p is 16-byte aligned
-template <class T>
-__device__ __forceinline__ void sh_load8(const T* p, int n, bool vec, float* x) {
-  if (vec && n == 8) {
-    if constexpr (sizeof(T) == 2) {
-      const uint4 q = __ldcs(reinterpret_cast<const uint4*>(p));
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      }
-    } else {
-      const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
-      const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-      x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = j < n ? sh_to_float<T>(p[j]) : 0.f;
-  }
+// packed pairs of fp32 (one instruction for two columns)
+__device__ __forceinline__ float2 sh_fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 sh_add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 sh_mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 
+template <int V>
+struct ShInt {
+  static constexpr int value = V;
+};
+
+// Eight columns as they lie in memory: 4 words of bf16 pairs or 8 of fp32.
 template <class T>
-__device__ __forceinline__ void sh_store8(T* p, int n, bool vec, const float* x) {
-  if (vec && n == 8) {
-    if constexpr (sizeof(T) == 2) {
-      uint32_t w[4];
+struct ShRaw {
+  static constexpr int N = sizeof(T) * 2;
+  uint32_t w[N];
+};
+// columns 2i, 2i + 1
+__device__ __forceinline__ float2 sh_pair(const ShRaw<__nv_bfloat16>& r, int i) {
+  return make_float2(__uint_as_float(r.w[i] << 16), __uint_as_float(r.w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ float2 sh_pair(const ShRaw<float>& r, int i) {
+  return make_float2(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1]));
+}
+__device__ __forceinline__ void sh_put(ShRaw<__nv_bfloat16>& r, int i, float2 v) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+  r.w[i] = *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void sh_put(ShRaw<float>& r, int i, float2 v) {
+  r.w[2 * i] = __float_as_uint(v.x);
+  r.w[2 * i + 1] = __float_as_uint(v.y);
+}
+
+// bytes of x picked by the selector's nibbles; a nibble of 8 + i gives byte i's sign, eight times
+template <uint32_t SEL>
+__device__ __forceinline__ uint32_t sh_signs(uint32_t x) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(d) : "r"(x), "n"(SEL));
+  return d;
+}
+
+// Sets the columns whose bit in `bar` is 1 to a bit pattern (of both halves of a
+// word for bf16).  bf16: the bits of four columns are spread to the top bits of
+// four bytes by one multiplication (their copies do not meet), and each byte's
+// top bit is replicated over a 16-bit half by a byte permutation.
+__device__ __forceinline__ void sh_fill(ShRaw<__nv_bfloat16>& r, uint32_t bar, uint32_t pattern) {
+  constexpr uint32_t SPREAD = (1u << 7) | (1u << 14) | (1u << 21) | (1u << 28);
+  const uint32_t lo = (bar & 15u) * SPREAD, hi = (bar >> 4) * SPREAD;
+  const uint32_t m[4] = {sh_signs<0x9988>(lo), sh_signs<0xbbaa>(lo), sh_signs<0x9988>(hi), sh_signs<0xbbaa>(hi)};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        w[i] = *reinterpret_cast<uint32_t*>(&h);
-      }
-      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-      reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-      reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  for (int i = 0; i < 4; ++i) r.w[i] = (r.w[i] & ~m[i]) | (pattern & m[i]);
+}
+__device__ __forceinline__ void sh_fill(ShRaw<float>& r, uint32_t bar, uint32_t pattern) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) r.w[e] = ((bar >> e) & 1u) ? pattern : r.w[e];
+}
+template <class T>
+constexpr uint32_t sh_minus_inf() { return sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u; }
+
+// the warp's maximum, NaN left out
+__device__ __forceinline__ float sh_warp_max(float x) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+  return m;
+}
+// Copies 16 bytes (or the first `bytes` of them, the rest zero) to shared memory, asynchronously.
+__device__ __forceinline__ void sh_copy16(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void sh_copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void sh_copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// N words that start `shift` bytes (even, below 16; the same for the warp) after
+// the 16-byte boundary p.
+template <int N>
+__device__ __forceinline__ void sh_read(uint32_t* w, const uint8_t* p, int shift) {
+  uint32_t v[N + 4];
+#pragma unroll
+  for (int q = 0; q < (N + 4) / 4; ++q) {
+    if (q < N / 4 || shift) {
+      const uint4 t = *(reinterpret_cast<const uint4*>(p) + q);
+      v[4 * q] = t.x, v[4 * q + 1] = t.y, v[4 * q + 2] = t.z, v[4 * q + 3] = t.w;
     }
-  } else {
+  }
+  if (shift == 0) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < n) p[j] = sh_from_float<T>(x[j]);
+    for (int i = 0; i < N; ++i) w[i] = v[i];
+    return;
+  }
+  const auto pick = [&](auto at) {
+    constexpr int W = decltype(at)::value;
+    if (shift & 2) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[i] = __funnelshift_r(v[i + W], v[i + W + 1 < N + 4 ? i + W + 1 : N + 3], 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[i] = v[i + W];
+    }
+  };
+  switch (shift >> 2) {
+    case 0: pick(ShInt<0>{}); break;
+    case 1: pick(ShInt<1>{}); break;
+    case 2: pick(ShInt<2>{}); break;
+    default: pick(ShInt<3>{}); break;
   }
 }
 
@@ -130,101 +245,208 @@ __device__ __forceinline__ bool sh_positive(float x) { return x > 0.f && x < INF
 template <int MODE>
 __device__ __forceinline__ bool sh_load_row(const ShapeArgs& a, int row, ShRow& r, int& bad) {
   const gh_shaping& s = a.s;
+  // every load is issued before the first is used
+  const bool on = MODE == SHAPE_OUT || a.mask[row] != 0;
+  const int y = MODE == SHAPE_OUT ? -1 : a.targets[row];
+  const float coef = MODE == SHAPE_GRAD ? a.coef[row] : 1.f;
+  const float lse = MODE == SHAPE_GRAD ? a.lse[row] : 0.f;
+  const float rep = s.repetition ? s.repetition[row] : 1.f;
+  const float pres = s.presence ? s.presence[row] : 0.f;
+  const float freq = s.frequency ? s.frequency[row] : 0.f;
+  const float temp = s.temperature ? s.temperature[row] : 1.f;
+  const long long begin = s.hist_len ? s.hist_begin[row] : 0;
+  const int len = s.hist_len ? s.hist_len[row] : 0;
+  const int plen = s.hist_len && s.prompt_len ? s.prompt_len[row] : 0;
+  const int set = s.bias_set ? s.bias_set[row] : -1;
+  const int allow = s.allow_row ? s.allow_row[row] : -1;
   bad = 0;
-  bool live = true;
-  r.y = -1;
-  r.scale = 0.f;
-  r.lse = 0.f;
-  if (MODE != SHAPE_OUT) {
-    live = a.mask[row] != 0;
-    r.y = a.targets[row];
-  }
-  if (MODE == SHAPE_GRAD) {
-    const float c = a.coef[row];
-    live = live && c != 0.f && a.lse[row] != -INFINITY;  // -inf: the mask leaves nothing, the gradient is 0
-    r.scale = (a.grad_out ? *a.grad_out : 1.f) * c;
-    r.lse = a.lse[row];
-  }
-  r.begin = 0;
-  r.len = r.plen = 0;
-  r.rep = s.repetition ? s.repetition[row] : 1.f;
-  r.pres = s.presence ? s.presence[row] : 0.f;
-  r.freq = s.frequency ? s.frequency[row] : 0.f;
-  float t = s.temperature ? s.temperature[row] : 1.f;
-  if (!sh_positive(r.rep)) r.rep = 1.f, bad = 1;
-  if (!sh_positive(t)) t = 1.f, bad = 1;
-  r.inv_rep = 1.f / r.rep;
-  r.inv_t = 1.f / t;
-  if (s.hist_len && (r.rep != 1.f || r.pres != 0.f || r.freq != 0.f)) {
-    const long long b = s.hist_begin[row];
-    const int n = s.hist_len[row];
-    if (b < 0 || n < 0 || n > SHAPE_MAX_HIST || b > s.num_tokens - n) {
+  r.bias_b = r.bias_e = 0;
+  if (set < -1 || set >= s.num_bias_sets) {
+    bad = set != -1;
+  } else if (set >= 0) {
+    const int b = s.bias_offsets[set], e = s.bias_offsets[set + 1];
+    if (b < 0 || e < b || e > s.num_bias || e - b > SHAPE_MAX_BIAS) {
       bad = 1;
-    } else if (n > 0) {
-      r.begin = b;
-      r.len = n;
-      const int p = s.prompt_len ? s.prompt_len[row] : 0;
-      r.plen = p < 0 ? 0 : (p < n ? p : n);
+    } else if (e > b) {
+      r.bias_b = b;
+      r.bias_e = e;
     }
   }
-  r.bias_b = r.bias_e = 0;
-  if (s.bias_set) {
-    const int k = s.bias_set[row];
-    if (k >= s.num_bias_sets || k < -1) {
+  r.y = y;
+  r.rep = sh_positive(rep) ? rep : 1.f;
+  r.pres = pres;
+  r.freq = freq;
+  const float t = sh_positive(temp) ? temp : 1.f;
+  if (!sh_positive(rep) || !sh_positive(temp)) bad = 1;
+  r.inv_rep = 1.f / r.rep;
+  r.inv_t = 1.f / t;
+  r.lse = lse;
+  r.scale = MODE == SHAPE_GRAD ? (a.grad_out ? *a.grad_out : 1.f) * coef * r.inv_t : 0.f;
+  r.begin = 0;
+  r.len = r.plen = 0;
+  if (r.rep != 1.f || pres != 0.f || freq != 0.f) {
+    if (begin < 0 || len < 0 || len > SHAPE_MAX_HIST || begin > s.num_tokens - len) {
       bad = 1;
-    } else if (k >= 0) {
-      const int b = s.bias_offsets[k], e = s.bias_offsets[k + 1];
-      if (b < 0 || e < b || e > s.num_bias || e - b > SHAPE_MAX_BIAS) {
-        bad = 1;
-      } else if (e > b) {
-        r.bias_b = b;
-        r.bias_e = e;
-      }
+    } else if (len > 0) {
+      r.begin = begin;
+      r.len = len;
+      r.plen = plen < 0 ? 0 : (plen < len ? plen : len);
     }
   }
   r.allow = -1;
-  if (s.allow_row) {
-    const int k = s.allow_row[row];
-    if (k >= s.num_allow || k < -1)
-      bad = 1;
-    else
-      r.allow = k;
-  }
-  return live;
+  if (allow < -1 || allow >= s.num_allow)
+    bad |= allow != -1;
+  else
+    r.allow = allow;
+  // GRAD: with an LSE of -inf the mask leaves nothing, and the gradient is 0
+  return on && coef != 0.f && lse != -INFINITY;
 }
 
-// Adds history tokens [from, to) of the row that fall into [c0, c0 + cols) to the words.
-__device__ __forceinline__ void sh_add_tokens(const int32_t* tokens, const ShRow& r, int from, int to, int c0, int cols,
-                                              uint32_t* word, uint32_t* used) {
-  const int32_t* h = tokens + r.begin;
-#pragma unroll 4
-  for (int k = from + threadIdx.x; k < to; k += SH_THREADS) {
+// The ranked set of a range of columns.  `member` and `before` stay as built;
+// `active` has the members whose word is in use by the present row (the others
+// belong to later rows of the chain).
+struct ShSet {
+  uint32_t* member;  // [cols / 32]
+  uint32_t* active;  // [cols / 32]
+  uint32_t* word;    // [SH_SET]
+  uint16_t* before;  // [cols / 32] members before each 32 columns
+  __device__ __forceinline__ uint32_t rank(uint32_t j) const {
+    return before[j >> 5] + __popc(member[j >> 5] & ((1u << (j & 31)) - 1u));
+  }
+};
+
+// one history token, as the k-th of its row
+__device__ __forceinline__ void sh_count(const ShSet& set, uint32_t j, bool prompt) {
+  uint32_t* w = set.word + set.rank(j);
+  if (prompt)
+    atomicOr(w, SH_PROMPT);
+  else
+    atomicAdd(w, 1u);
+  atomicOr(&set.active[j >> 5], 1u << (j & 31));
+}
+
+// Builds the set of columns [c0, c0 + cols) from the history of `last`, the
+// chain's last row, with the words of `first`, its first.  Called by the whole
+// CTA.  `clean`: member is zero and nothing is in use.  Returns the number of
+// members; above SH_SET nothing but `member` is set.
+__device__ int sh_build(const ShapeArgs& a, const ShSet& set, const ShRow& first, const ShRow& last, int c0, int cols,
+                        bool clean, int* warp_sum) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int nw = (cols + 31) / 32;
+  if (!clean) {
+    __syncthreads();  // the set before this one is done with
+    for (int i = tid; i < nw; i += SH_THREADS) set.member[i] = 0;
+    __syncthreads();
+  }
+  const int32_t* h = a.s.tokens + last.begin;
+#pragma unroll 8
+  for (int k = tid; k < last.len; k += SH_THREADS) {
     const uint32_t j = static_cast<uint32_t>(h[k] - c0);
-    if (j < static_cast<uint32_t>(cols)) {
-      if (k < r.plen)
-        atomicOr(&word[j], SH_PROMPT);
-      else
-        atomicAdd(&word[j], 1u);
-      atomicOr(&used[j >> 5], 1u << (j & 31));
-    }
+    if (j < static_cast<uint32_t>(cols)) atomicOr(&set.member[j >> 5], 1u << (j & 31));
   }
+  for (int k = last.bias_b + tid; k < last.bias_e; k += SH_THREADS) {
+    const uint32_t j = static_cast<uint32_t>(a.s.bias_tokens[k] - c0);
+    if (j < static_cast<uint32_t>(cols)) atomicOr(&set.member[j >> 5], 1u << (j & 31));
+  }
+  __syncthreads();
+  // ranks: each thread a run of words, then the runs before it
+  const int run = (nw + SH_THREADS - 1) / SH_THREADS;
+  const int i0 = min(tid * run, nw), i1 = min(i0 + run, nw);
+  int n = 0;
+  for (int i = i0; i < i1; ++i) n += __popc(set.member[i]);
+  int incl = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  int off = incl - n, total = 0;
+#pragma unroll
+  for (int w = 0; w < SH_WARPS; ++w) {
+    if (w < warp) off += warp_sum[w];
+    total += warp_sum[w];
+  }
+  if (total > SH_SET) return total;
+  for (int i = i0; i < i1; ++i) {
+    set.before[i] = static_cast<uint16_t>(off);
+    off += __popc(set.member[i]);
+    set.active[i] = 0;
+  }
+  for (int i = tid; i < total; i += SH_THREADS) set.word[i] = 0;
+  __syncthreads();
+  if (first.bias_e > first.bias_b) {
+    for (int k = first.bias_b + tid; k < first.bias_e; k += SH_THREADS) {
+      const uint32_t j = static_cast<uint32_t>(a.s.bias_tokens[k] - c0);
+      if (j < static_cast<uint32_t>(cols)) {
+        // the last entry of a token counts
+        atomicMax(&set.word[set.rank(j)], static_cast<uint32_t>(k - first.bias_b + 1) << SH_BIAS_SHIFT);
+        atomicOr(&set.active[j >> 5], 1u << (j & 31));
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll 8
+  for (int k = tid; k < first.len; k += SH_THREADS) {
+    const uint32_t j = static_cast<uint32_t>(h[k] - c0);
+    if (j < static_cast<uint32_t>(cols)) sh_count(set, j, k < first.plen);
+  }
+  __syncthreads();
+  return total;
 }
 
-template <class TIn, class TOut, int MODE>
-__global__ void __launch_bounds__(SH_THREADS, 3) shape_kernel(const ShapeArgs a) {
+// The parameters of a row that the members need.
+struct ShPen {
+  float rep, inv_rep, pres, freq;
+  const float* bias;  // the row's list, one entry before its first
+};
+// A member's shaped value before the temperature, and its slope times T.
+__device__ __forceinline__ float sh_member(const ShPen& p, uint32_t w, float x, float& slope) {
+  const uint32_t c = w & SH_COUNT;
+  slope = (w & (SH_COUNT | SH_PROMPT)) ? (x > 0.f ? p.inv_rep : p.rep) : 1.f;
+  x = x * slope - (c ? fmaf(p.freq, static_cast<float>(c), p.pres) : 0.f);
+  const uint32_t b = w >> SH_BIAS_SHIFT;
+  if (b) x += __ldg(p.bias + b);
+  return x;
+}
+
+// Shared memory of a CTA: the set, then each warp's stages and (unaligned
+// outputs) its output tile.
+constexpr int SH_STAGES = 2;
+constexpr int SH_TILE = 2048 + 16;  // a segment and the 16 bytes that an unaligned one is longer
+
+// ALIGNED: rows of the logits start on 16-byte boundaries.  OUT_TILE: rows of the
+// output do not, and go through shared memory (types of one size).  Neither: the
+// output is written element by element where its rows are not aligned.
+// MASKS: rows may carry an allow mask.
+template <class TIn, class TOut, int MODE, bool ALIGNED, bool OUT_TILE, bool MASKS>
+__global__ void __launch_bounds__(SH_THREADS, OUT_TILE ? 2 : SH_CTAS) shape_kernel(const ShapeArgs a) {
+  using S = ShSeg<TIn>;
+  constexpr int CB = 256 * sizeof(TIn);  // bytes of a chunk
   extern __shared__ __align__(16) uint8_t sh_smem[];
   __shared__ ShRow rows[SH_MAX_ROWS];
   __shared__ uint32_t live_bits;
-  uint32_t* word = reinterpret_cast<uint32_t*>(sh_smem);
-  uint32_t* used = word + (a.table ? a.cols : 0);
+  __shared__ int warp_sum[SH_WARPS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  ShSet set;
+  set.member = reinterpret_cast<uint32_t*>(sh_smem);
+  set.active = set.member + a.cols / 32;
+  set.word = set.active + a.cols / 32;
+  set.before = reinterpret_cast<uint16_t*>(set.word + SH_SET);
+  uint8_t* const tiles = reinterpret_cast<uint8_t*>(set.before + a.cols / 32);
+  uint8_t* const ring = tiles + warp * (SH_STAGES * SH_TILE);
+  uint8_t* const out_tile = tiles + SH_WARPS * (SH_STAGES * SH_TILE) + warp * SH_TILE;
   const int tile = static_cast<int>(blockIdx.x % a.ntiles);
   const int row0 = static_cast<int>(blockIdx.x / a.ntiles) * a.rows_per_cta;
   const int nrows = min(a.rows_per_cta, a.R - row0);
   const int V = a.V;
-  const int c0 = tile * a.cols;
-  const int cols = min(a.cols, V - c0);
+  const int t0 = tile * a.cols, tcols = min(a.cols, V - t0);
+  // the bytes that belong to the logits
+  const uint8_t* const first_byte = static_cast<const uint8_t*>(a.logits);
+  const uint8_t* const end_byte = first_byte + (static_cast<size_t>(a.R - 1) * a.ld + V) * sizeof(TIn);
 
+  for (int i = tid; i < a.cols / 32; i += SH_THREADS) set.member[i] = 0;
   if (warp == 0) {
     ShRow r;
     int bad = 0;
@@ -232,8 +454,8 @@ __global__ void __launch_bounds__(SH_THREADS, 3) shape_kernel(const ShapeArgs a)
     if (lane < nrows) live = sh_load_row<MODE>(a, row0 + lane, r, bad);
     if (bad && live && tile == 0) atomicOr(a.status, GH_DEV_BAD_ROW);
     const uint32_t bits = __ballot_sync(0xffffffffu, live);
-    const uint32_t before = bits & ((1u << lane) - 1u);
-    const int prev = before ? 31 - __clz(before) : 0;
+    const uint32_t earlier = bits & ((1u << lane) - 1u);
+    const int prev = earlier ? 31 - __clz(earlier) : 0;
     const long long pb = __shfl_sync(0xffffffffu, r.begin, prev);
     const int pl = __shfl_sync(0xffffffffu, r.len, prev);
     const int pp = __shfl_sync(0xffffffffu, r.plen, prev);
@@ -241,19 +463,19 @@ __global__ void __launch_bounds__(SH_THREADS, 3) shape_kernel(const ShapeArgs a)
     const int p1 = __shfl_sync(0xffffffffu, r.bias_e, prev);
     if (live) {
       r.tab = TAB_BUILD;
-      r.add_from = 0;
+      r.add = 0;
       if (r.len == 0 && r.bias_e == r.bias_b) {
         r.tab = TAB_NONE;
-      } else if (before && (pl > 0 || p1 > p0) && p0 == r.bias_b && p1 == r.bias_e && pb == r.begin && pl <= r.len &&
-          min(pp, pl) == min(r.plen, pl)) {
+      } else if (earlier && (pl > 0 || p1 > p0) && p0 == r.bias_b && p1 == r.bias_e && pl <= r.len &&
+                 (pl == 0 || pb == r.begin) && min(pp, pl) == min(r.plen, pl)) {
         if (pl == r.len) {
           r.tab = TAB_KEEP;
         } else if (pl + 1 == r.len && pl >= r.plen) {
           r.tab = TAB_ADD1;
-          r.add_from = a.s.tokens[r.begin + pl];
+          r.add = a.s.tokens[r.begin + pl];
         } else {
           r.tab = TAB_ADD;
-          r.add_from = pl;
+          r.add = pl;
         }
       }
       rows[lane] = r;
@@ -261,163 +483,394 @@ __global__ void __launch_bounds__(SH_THREADS, 3) shape_kernel(const ShapeArgs a)
     if (lane == 0) live_bits = bits;
   }
   __syncthreads();
-  const uint32_t bits = live_bits;
 
-  for (int rr = 0; rr < nrows; ++rr) {
-    const int row = row0 + rr;
-    TOut* out = MODE == SHAPE_LOGP ? nullptr : reinterpret_cast<TOut*>(a.out) + static_cast<size_t>(row) * a.out_ld + c0;
-    if (!((bits >> rr) & 1u)) {
-      if (MODE == SHAPE_GRAD) {
-        const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        for (int j = tid * 8; j < cols; j += SH_THREADS * 8) sh_store8<TOut>(out + j, min(8, cols - j), a.vec_out, zero);
-      }
-      continue;
+  if (MODE == SHAPE_GRAD) {
+    for (int rr = 0; rr < nrows; ++rr) {
+      if ((live_bits >> rr) & 1u) continue;
+      TOut* out = reinterpret_cast<TOut*>(a.out) + static_cast<size_t>(row0 + rr) * a.out_ld + t0;
+      // whole 16-byte words between the row's ends
+      const uintptr_t b = reinterpret_cast<uintptr_t>(out), e = b + tcols * sizeof(TOut);
+      const uintptr_t b16 = min((b + 15) & ~uintptr_t(15), e), e16 = max(e & ~uintptr_t(15), b16);
+      for (uintptr_t p = b16 + tid * 16; p < e16; p += SH_THREADS * 16)
+        __stcs(reinterpret_cast<uint4*>(p), make_uint4(0, 0, 0, 0));
+      for (uintptr_t p = b + tid * sizeof(TOut); p < b16; p += SH_THREADS * sizeof(TOut))
+        *reinterpret_cast<TOut*>(p) = sh_from_float<TOut>(0.f);
+      for (uintptr_t p = e16 + tid * sizeof(TOut); p < e; p += SH_THREADS * sizeof(TOut))
+        *reinterpret_cast<TOut*>(p) = sh_from_float<TOut>(0.f);
     }
-    const ShRow& r = rows[rr];
-    {
-      const int tab = r.tab;
-      if (tab == TAB_BUILD) {
-        __syncthreads();
-        for (int j = tid * 4; j < a.cols; j += SH_THREADS * 4) *reinterpret_cast<uint4*>(word + j) = make_uint4(0, 0, 0, 0);
-        for (int j = tid; j < a.cols / 32; j += SH_THREADS) used[j] = 0;
-        __syncthreads();
-        if (r.bias_e > r.bias_b) {
-          for (int k = r.bias_b + tid; k < r.bias_e; k += SH_THREADS) {
-            const uint32_t j = static_cast<uint32_t>(a.s.bias_tokens[k] - c0);
-            if (j < static_cast<uint32_t>(cols)) {
-              // the last entry of a token counts
-              atomicMax(&word[j], static_cast<uint32_t>(k - r.bias_b + 1) << SH_BIAS_SHIFT);
-              atomicOr(&used[j >> 5], 1u << (j & 31));
-            }
-          }
-          __syncthreads();
-        }
-        sh_add_tokens(a.s.tokens, r, 0, r.len, c0, cols, word, used);
-        __syncthreads();
-      } else if (tab == TAB_ADD) {
-        __syncthreads();
-        sh_add_tokens(a.s.tokens, r, r.add_from, r.len, c0, cols, word, used);
-        __syncthreads();
-      } else if (tab == TAB_ADD1) {
-        const uint32_t j = static_cast<uint32_t>(r.add_from - c0);
-        if (j < static_cast<uint32_t>(cols)) {  // the same for every thread: read from shared memory
-          __syncthreads();
-          if (tid == 0) {
-            word[j] += 1u;
-            used[j >> 5] |= 1u << (j & 31);
-          }
-          __syncthreads();
-        }
-      }
-    }
+  }
 
-    const TIn* in = reinterpret_cast<const TIn*>(a.logits) + static_cast<size_t>(row) * a.ld + c0;
-    const uint8_t* allow =
-        r.allow >= 0 ? reinterpret_cast<const uint8_t*>(a.s.allow_bits + static_cast<size_t>(r.allow) * ((V + 31) / 32)) + (c0 >> 3)
-                     : nullptr;
-    for (int seg = warp * SH_SEG; seg < cols; seg += SH_WARPS * SH_SEG) {
-      float x[SH_CHUNKS][8];
-      uint32_t ok[SH_CHUNKS];
-#pragma unroll
-      for (int u = 0; u < SH_CHUNKS; ++u) {
-        const int j = seg + u * 256 + lane * 8;
-        const int n = min(8, cols - j);
-        ok[u] = n <= 0 ? 0u : (n < 8 ? (1u << n) - 1u : 0xffu);
-        if (allow && n > 0) ok[u] &= allow[j >> 3];
-      }
-#pragma unroll
-      for (int u = 0; u < SH_CHUNKS; ++u) {
-        const int j = seg + u * 256 + lane * 8;
-        if (ok[u]) {
-          sh_load8<TIn>(in + j, min(8, cols - j), a.vec_in, x[u]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[u][e] = 0.f;
+  const size_t allow_ld = static_cast<size_t>((V + 31) / 32);
+  uint32_t todo = live_bits;
+  bool clean = true;
+  while (todo) {
+    // the next chain: rows `chain`, first to last
+    const int head = __ffs(todo) - 1;
+    uint32_t chain = 1u << head;
+    const bool ranked = rows[head].tab != TAB_NONE;
+    int last = head;
+    for (uint32_t rest = todo & (todo - 1); rest; rest &= rest - 1) {
+      const int q = __ffs(rest) - 1;
+      const int tab = rows[q].tab;
+      if (tab == TAB_BUILD || (tab == TAB_NONE) == ranked) break;
+      chain |= 1u << q;
+      last = q;
+    }
+    todo &= ~chain;
+
+    int width = tcols;  // columns of a pass: all of them unless the set has too many members
+    for (int c0 = t0; c0 < t0 + tcols; c0 += width) {
+      int cols = min(width, t0 + tcols - c0);
+      int nseg = (cols + S::COLS - 1) / S::COLS;
+      // The copies run SH_STAGES - 1 segments ahead of the present one, the reads
+      // of the allow bits one more: `oks` has them (a byte per chunk) from the
+      // present segment to the one copied next.  `left`: the chain's rows from the
+      // iterator's on.
+      uint32_t left_c = 0, oks[SH_STAGES];
+      int seg_c = 0, stage_c;
+      const uint8_t* src_c = nullptr;    // the segment of the copies' iterator in the logits
+      const uint8_t* allow_c = nullptr;  // its row's allow bits from c0 on, if any
+      const auto row_c = [&] {           // the iterator enters a row
+        const int rr = __ffs(left_c) - 1;
+        src_c = first_byte + (static_cast<size_t>(row0 + rr) * a.ld + (c0 + warp * S::COLS)) * sizeof(TIn);
+        const int k = MASKS ? rows[rr].allow : -1;
+        allow_c = k < 0 ? nullptr : reinterpret_cast<const uint8_t*>(a.s.allow_bits + k * allow_ld) + (c0 >> 3);
+        seg_c = warp;
+      };
+      const auto next_c = [&] {
+        seg_c += SH_WARPS;
+        src_c += SH_WARPS * S::COLS * sizeof(TIn);
+        if (seg_c >= nseg) {
+          left_c &= left_c - 1;
+          if (left_c) row_c();
         }
-      }
-      uint32_t seen[SH_CHUNKS], pos[SH_CHUNKS];  // GRAD: columns whose slope is theta or 1 / theta
+      };
+      const auto load_ok = [&] {
+        if ((!MASKS || !allow_c) && (seg_c + 1) * S::COLS <= cols) return S::FULL;
+        if (!left_c) return 0u;
+        uint32_t ok = 0;
+        const int j0 = seg_c * S::COLS + lane * 8;
 #pragma unroll
-      for (int u = 0; u < SH_CHUNKS; ++u) {
-        const int j = seg + u * 256 + lane * 8;
-        seen[u] = pos[u] = 0;
-        uint32_t t = 0;
-        if (r.tab != TAB_NONE && ok[u]) t = reinterpret_cast<const uint8_t*>(used)[j >> 3] & ok[u];
-        if (t) {
+        for (int u = 0; u < S::CHUNKS; ++u) {
+          const int j = j0 + u * 256, n = cols - j;
+          uint32_t o = n <= 0 ? 0u : (n < 8 ? (1u << n) - 1u : 0xffu);
+          if (MASKS && allow_c && n > 0) o &= __ldg(allow_c + (j >> 3));
+          ok |= o << (8 * u);
+        }
+        return ok;
+      };
+      // copies a segment's 16-byte words; `ok` is of this lane's columns
+      const auto copy = [&](uint32_t ok, uint8_t* dst) {
+        if (left_c) {
+          if (ALIGNED) {
+            const uint8_t* from = src_c + lane * 16 * S::LANE16;
+            uint8_t* to = dst + lane * 16 * S::LANE16;
+            if (ok == S::FULL) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if ((t >> e) & 1u) {
-              const uint32_t w = word[j + e];
-              const uint32_t c = w & SH_COUNT;
-              float v = x[u][e];
-              if (w & (SH_COUNT | SH_PROMPT)) {
-                seen[u] |= 1u << e;
-                if (v > 0.f) pos[u] |= 1u << e;
-                v *= v > 0.f ? r.inv_rep : r.rep;
+              for (int q = 0; q < 4; ++q) {
+                const int at = (q / S::LANE16) * CB + (q % S::LANE16) * 16;
+                sh_copy16(to + at, from + at, 16);
               }
-              v -= r.freq * static_cast<float>(c);
-              if (c) v -= r.pres;
-              const uint32_t be = w >> SH_BIAS_SHIFT;
-              if (be) v += __ldg(a.s.bias_values + r.bias_b + be - 1);
-              x[u][e] = v;
+            } else {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const int u = q / S::LANE16, at = u * CB + (q % S::LANE16) * 16;
+                const ptrdiff_t rest = end_byte - (from + at);
+                if ((ok >> (8 * u)) & 0xffu)
+                  sh_copy16(to + at, from + at, rest >= 16 ? 16 : (rest > 0 ? static_cast<int>(rest) : 0));
+              }
             }
-          }
-        }
-      }
-      if (MODE == SHAPE_LOGP) {
-        float m = -INFINITY;
-#pragma unroll
-        for (int u = 0; u < SH_CHUNKS; ++u) {
-          const int j = seg + u * 256 + lane * 8;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[u][e] = ((ok[u] >> e) & 1u) ? x[u][e] : -INFINITY;
-          const int rel = r.y - (c0 + j);
-          if (static_cast<uint32_t>(rel) < 8u && r.y < V) {
-            float z = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) z = e == rel ? x[u][e] : z;
-            a.zy[row] = z * r.inv_t;
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) m = fmaxf(m, x[u][e]);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        // the maximum of the raw values is that of the scaled ones; the difference is taken before the step to base
-        // 2, where a row of the type's lowest value would overflow
-        m *= r.inv_t;
-        const float ref = m == -INFINITY ? 0.f : m;
-        float sum = 0.f;
-#pragma unroll
-        for (int u = 0; u < SH_CHUNKS; ++u)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) sum += ex2_approx(fmaf(x[u][e], r.inv_t, -ref) * SH_LOG2E);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) a.part[static_cast<size_t>(row) * a.nseg + (c0 + seg) / SH_SEG] = make_float2(m, sum);
-      } else {
-#pragma unroll
-        for (int u = 0; u < SH_CHUNKS; ++u) {
-          const int j = seg + u * 256 + lane * 8;
-          const int n = min(8, cols - j);
-          if (n <= 0) continue;
-          float o[8];
-          if (MODE == SHAPE_OUT) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = ((ok[u] >> e) & 1u) ? x[u][e] * r.inv_t : -INFINITY;
           } else {
-            const int rel = r.y - (c0 + j);
-            const float g = r.scale * r.inv_t;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float p = ex2_approx(fmaf(x[u][e], r.inv_t, -r.lse) * SH_LOG2E);
-              float d = g * ((e == rel ? 1.f : 0.f) - p);
-              if ((seen[u] >> e) & 1u) d *= ((pos[u] >> e) & 1u) ? r.inv_rep : r.rep;
-              o[e] = ((ok[u] >> e) & 1u) ? d : 0.f;
+            // from the boundary before the segment, up to 129 words; those that reach out of the logits are copied by
+            // element
+            const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(src_c) & 15);
+            const uint8_t* from = src_c - shift;
+            const int bytes = min(cols - seg_c * S::COLS, S::COLS) * static_cast<int>(sizeof(TIn)) + shift;
+            for (int at = lane * 16; at < bytes; at += 512) {
+              if (from + at >= first_byte && from + at + 16 <= end_byte) {
+                sh_copy16(dst + at, from + at, 16);
+              } else {
+                for (int e = 0; e < 16; e += static_cast<int>(sizeof(TIn)))
+                  if (from + at + e >= first_byte && from + at + e < end_byte)
+                    *reinterpret_cast<TIn*>(dst + at + e) = *reinterpret_cast<const TIn*>(from + at + e);
+              }
             }
           }
-          sh_store8<TOut>(out + j, n, a.vec_out, o);
+        }
+        sh_copy_commit();
+      };
+      const auto start = [&] {
+        left_c = warp < nseg ? chain : 0u;
+        if (left_c) row_c();
+#pragma unroll
+        for (int k = 0; k < SH_STAGES; ++k) {
+          oks[k] = load_ok();
+          if (k < SH_STAGES - 1) {
+            copy(oks[k], ring + k * SH_TILE);
+            if (left_c) next_c();
+          }
+        }
+        stage_c = SH_STAGES - 1;
+      };
+      start();  // the first copies are under way while the set is built
+      if (ranked) {
+        int members = sh_build(a, set, rows[head], rows[last], c0, cols, clean, warp_sum);
+        clean = false;
+        while (members > SH_SET) {
+          // a share of the columns that should hold SH_SET of these members, or SH_SET columns, which do
+          const int64_t fit = static_cast<int64_t>(cols) * SH_SET / members * 4 / 5 / 1024 * 1024;
+          width = cols = width == cols && fit > SH_SET ? static_cast<int>(fit) : SH_SET;
+          nseg = (cols + S::COLS - 1) / S::COLS;
+          sh_copy_wait<0>();
+          __syncwarp();
+          start();
+          members = sh_build(a, set, rows[head], rows[last], c0, cols, false, warp_sum);
         }
       }
+
+      int stage = 0;  // of the present segment
+      for (uint32_t left = warp < nseg ? chain : 0u; left; left &= left - 1) {
+      const int rr = __ffs(left) - 1, row = row0 + rr;
+      const ShRow& r = rows[rr];
+      const int allow = MASKS ? r.allow : -1;
+      // the target, as a column of this range, and its segment
+      const int y = MODE != SHAPE_OUT && r.y >= c0 && r.y < c0 + cols ? r.y - c0 : -1;
+      const int ysg = y < 0 ? -1 : y / S::COLS;
+      float2* const part = MODE == SHAPE_LOGP ? a.part + static_cast<size_t>(row) * a.nseg + c0 / S::COLS : nullptr;
+      const float inv_t = r.inv_t, lse = r.lse, scale = r.scale;
+      const ShPen pen{r.rep, r.inv_rep, r.pres, r.freq, a.s.bias_values + (r.bias_b - 1)};
+      if (rr != head && (r.tab == TAB_ADD1 || r.tab == TAB_ADD)) {
+        // the row's new tokens among this warp's columns
+        const bool one = r.tab == TAB_ADD1;
+        for (int k = (one ? r.len - 1 : r.add) + lane; k < r.len; k += 32) {
+          const uint32_t j = static_cast<uint32_t>((one ? r.add : a.s.tokens[r.begin + k]) - c0);
+          if (j < static_cast<uint32_t>(cols) && static_cast<int>(j / S::COLS) % SH_WARPS == warp)
+            sh_count(set, j, k < r.plen);
+        }
+        __syncwarp();
+      }
+      for (int sg = warp; sg < nseg; sg += SH_WARPS) {
+        const int seg = sg * S::COLS;
+        sh_copy_wait<SH_STAGES - 2>();
+        __syncwarp();  // every lane's part has landed, and the stage before is read
+        copy(oks[SH_STAGES - 1], ring + stage_c * SH_TILE);
+        if (left_c) next_c();
+        const uint32_t ok = oks[0];
+#pragma unroll
+        for (int k = 0; k < SH_STAGES - 1; ++k) oks[k] = oks[k + 1];
+        oks[SH_STAGES - 1] = load_ok();
+        const bool whole = seg + S::COLS <= cols;
+        uint8_t* const buf = ring + stage * SH_TILE;
+        stage = stage == SH_STAGES - 1 ? 0 : stage + 1;
+        stage_c = stage_c == SH_STAGES - 1 ? 0 : stage_c + 1;
+        const int shift = ALIGNED ? 0
+                                  : static_cast<int>(reinterpret_cast<uintptr_t>(
+                                        first_byte + (static_cast<size_t>(row) * a.ld + (c0 + seg)) * sizeof(TIn)) & 15);
+        TIn* const x = reinterpret_cast<TIn*>(buf + shift);  // the segment's columns
+
+        // the members among this lane's 32 columns, and the target
+        const int w0 = sg * S::WORDS + lane;  // word of the set
+        uint32_t mine = 0, target = 0, allowed = 0xffffffffu;
+        if (ranked && lane < S::WORDS && (whole || w0 * 32 < cols)) mine = set.active[w0];
+        if (MODE != SHAPE_OUT && sg == ysg && (y >> 5) == w0) target = 1u << (y & 31);
+        if (MASKS && (mine | target) && allow >= 0)
+          allowed = __ldg(a.s.allow_bits + allow * allow_ld + ((c0 >> 5) + w0));
+        uint32_t visit = (mine | target) & allowed;
+        const bool sparse = (ranked || sg == ysg) && __any_sync(0xffffffffu, visit != 0);
+        // a member's word, by its bit: ranks follow on the members before this lane's columns
+        uint32_t base = 0, member = 0;
+        if (ranked && visit) {
+          base = set.before[w0];
+          member = set.member[w0];
+        }
+        const auto word_of = [&](uint32_t bit) {
+          return (mine & bit) ? set.word[base + __popc(member & (bit - 1u))] : 0u;
+        };
+
+        if (MODE == SHAPE_LOGP) {
+          if (MASKS && (target & ~allowed)) a.zy[row] = -INFINITY;
+          float ml = -INFINITY, sl = 0.f;
+          if (sparse) {
+            bool more = false;
+            while (visit) {
+              const uint32_t bit = visit & (0u - visit);
+              visit ^= bit;
+              TIn* const p = x + lane * 32 + __ffs(bit) - 1;
+              float slope;
+              const float z = sh_member(pen, word_of(bit), sh_to_float<TIn>(*p), slope) * inv_t;
+              if (bit & target) a.zy[row] = z;
+              if (bit & mine) {
+                *p = sh_from_float<TIn>(-INFINITY);
+                if (!more) {
+                  ml = z, sl = 1.f;
+                  more = true;
+                } else {
+                  // the lowest finite value in place of -inf, whose difference with itself is no number
+                  const float mn = fmaxf(fmaxf(ml, z), -SH_LOWEST);
+                  sl = sl * ex2_approx((ml - mn) * SH_LOG2E) + ex2_approx((z - mn) * SH_LOG2E);
+                  ml = mn;
+                }
+              }
+            }
+            __syncwarp();
+          }
+          const uint32_t bars = ok ^ S::FULL;
+          if ((MASKS || !whole) && __any_sync(0xffffffffu, bars != 0)) {
+            // barred columns to -inf, in the stage
+#pragma unroll
+            for (int u = 0; u < S::CHUNKS; ++u) {
+              const uint32_t bar = (bars >> (8 * u)) & 0xffu;
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if ((bar >> e) & 1u) x[u * 256 + lane * 8 + e] = sh_from_float<TIn>(-INFINITY);
+            }
+            __syncwarp();
+          }
+          ShRaw<TIn> raw[S::CHUNKS];
+#pragma unroll
+          for (int u = 0; u < S::CHUNKS; ++u) sh_read<ShRaw<TIn>::N>(raw[u].w, buf + u * CB + lane * 16 * S::LANE16, shift);
+          float m;
+          if constexpr (sizeof(TIn) == 2) {
+            __nv_bfloat162 h[S::CHUNKS * 4];
+#pragma unroll
+            for (int u = 0; u < S::CHUNKS; ++u)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) h[u * 4 + i] = *reinterpret_cast<const __nv_bfloat162*>(&raw[u].w[i]);
+#pragma unroll
+            for (int o = S::CHUNKS * 2; o > 0; o >>= 1)
+#pragma unroll
+              for (int i = 0; i < o; ++i) h[i] = __hmax2(h[i], h[i + o]);
+            m = fmaxf(__low2float(h[0]), __high2float(h[0]));
+          } else {
+            m = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < S::CHUNKS; ++u)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) m = fmaxf(m, __uint_as_float(raw[u].w[i]));
+          }
+          // 1 / T > 0: the maximum of the raw values is that of the scaled ones
+          m = sh_warp_max(fmaxf(m * inv_t, ml));
+          const float ref = fmaxf(m, -SH_LOWEST);
+          float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          if (fabsf(ref) < SH_BIG) {
+            const float k = inv_t * SH_LOG2E, c = -ref * SH_LOG2E;
+            const float2 k2 = make_float2(k, k), c2 = make_float2(c, c);
+#pragma unroll
+            for (int u = 0; u < S::CHUNKS; ++u)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float2 v = sh_fma2(sh_pair(raw[u], i), k2, c2);
+                acc[i & 1] = sh_add2(acc[i & 1], make_float2(ex2_approx(v.x), ex2_approx(v.y)));
+              }
+          } else {  // values near the type's lowest: the difference first
+#pragma unroll
+            for (int u = 0; u < S::CHUNKS; ++u)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float2 v = sh_pair(raw[u], i);
+                acc[0].x += ex2_approx(fmaf(v.x, inv_t, -ref) * SH_LOG2E);
+                acc[0].y += ex2_approx(fmaf(v.y, inv_t, -ref) * SH_LOG2E);
+              }
+          }
+          float sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+          if (sparse) sum += sl * ex2_approx((ml - ref) * SH_LOG2E);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          if (lane == 0) part[sg] = make_float2(m, sum);
+        } else {
+          TOut* const out = reinterpret_cast<TOut*>(a.out) + static_cast<size_t>(row) * a.out_ld + (c0 + seg);
+          const uint32_t bars = ok ^ S::FULL;
+          const bool barred = MASKS && __any_sync(0xffffffffu, bars != 0);
+          const bool small = fabsf(lse) < SH_BIG;
+          const float k = MODE == SHAPE_OUT ? inv_t : inv_t * SH_LOG2E, c = -lse * SH_LOG2E;
+          const float2 k2 = make_float2(k, k), c2 = make_float2(c, c), g2 = make_float2(-scale, -scale);
+#pragma unroll
+          for (int u = 0; u < S::CHUNKS; ++u) {
+            ShRaw<TIn> raw;
+            sh_read<ShRaw<TIn>::N>(raw.w, buf + u * CB + lane * 16 * S::LANE16, shift);
+            ShRaw<TOut> o;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float2 v = sh_pair(raw, i);
+              if (MODE == SHAPE_OUT) {
+                v = sh_mul2(v, k2);
+              } else {
+                if (small) {
+                  v = sh_fma2(v, k2, c2);
+                } else {  // the difference first
+                  v.x = fmaf(v.x, inv_t, -lse) * SH_LOG2E;
+                  v.y = fmaf(v.y, inv_t, -lse) * SH_LOG2E;
+                }
+                v = sh_mul2(make_float2(ex2_approx(v.x), ex2_approx(v.y)), g2);
+              }
+              sh_put(o, i, v);
+            }
+            if (barred) sh_fill(o, (bars >> (8 * u)) & 0xffu, MODE == SHAPE_OUT ? sh_minus_inf<TOut>() : 0u);
+            const int j = u * 256 + lane * 8, n = cols - seg - j;
+            if (OUT_TILE) {
+#pragma unroll
+              for (int q = 0; q < ShRaw<TOut>::N / 4; ++q)
+                *(reinterpret_cast<uint4*>(out_tile + j * sizeof(TOut)) + q) =
+                    make_uint4(o.w[4 * q], o.w[4 * q + 1], o.w[4 * q + 2], o.w[4 * q + 3]);
+            } else if (a.vec_out && (whole || n >= 8)) {
+#pragma unroll
+              for (int q = 0; q < ShRaw<TOut>::N / 4; ++q)
+                __stcs(reinterpret_cast<uint4*>(out + j) + q,
+                       make_uint4(o.w[4 * q], o.w[4 * q + 1], o.w[4 * q + 2], o.w[4 * q + 3]));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float2 v = sh_pair(o, i);
+                if (2 * i < n) out[j + 2 * i] = sh_from_float<TOut>(v.x);
+                if (2 * i + 1 < n) out[j + 2 * i + 1] = sh_from_float<TOut>(v.y);
+              }
+            }
+          }
+          if (sparse) {
+            __syncwarp();  // after the dense stores of the other lanes
+            while (visit) {
+              const uint32_t bit = visit & (0u - visit);
+              visit ^= bit;
+              const int j = lane * 32 + __ffs(bit) - 1;
+              float slope;
+              const float z = sh_member(pen, word_of(bit), sh_to_float<TIn>(x[j]), slope);
+              float v;
+              if (MODE == SHAPE_OUT) {
+                v = z * inv_t;
+              } else {
+                const float p = ex2_approx(fmaf(z, inv_t, -lse) * SH_LOG2E);
+                v = scale * slope * (((bit & target) ? 1.f : 0.f) - p);
+              }
+              if (OUT_TILE)
+                reinterpret_cast<TOut*>(out_tile)[j] = sh_from_float<TOut>(v);
+              else
+                out[j] = sh_from_float<TOut>(v);
+            }
+          }
+          if (OUT_TILE) {
+            __syncwarp();
+            // 16-byte words of the output, and the elements before and after them
+            const int n = min(cols - seg, S::COLS);
+            const uintptr_t b = reinterpret_cast<uintptr_t>(out), e = b + n * sizeof(TOut);
+            const int before = min(static_cast<int>(((16 - (b & 15)) & 15) / sizeof(TOut)), n);
+            const int words = static_cast<int>((e - (b + before * sizeof(TOut))) / 16);
+            const int after = before + words * 16 / static_cast<int>(sizeof(TOut));
+            const TOut* src = reinterpret_cast<const TOut*>(out_tile);
+            if (lane < before) out[lane] = src[lane];
+            for (int q = lane; q < words; q += 32) {
+              uint32_t w[4];
+              sh_read<4>(w, out_tile + q * 16, before * static_cast<int>(sizeof(TOut)));
+              __stcs(reinterpret_cast<uint4*>(out + before) + q, make_uint4(w[0], w[1], w[2], w[3]));
+            }
+            if (lane < n - after) out[after + lane] = src[after + lane];
+            __syncwarp();  // the output tile is free
+          }
+        }
+
+      }
+      }
+      sh_copy_wait<0>();
+      __syncwarp();  // the stages are free
     }
   }
 }
@@ -470,15 +923,27 @@ __global__ void __launch_bounds__(256) shaped_merge_kernel(const ShapeArgs a) {
   }
 }
 
-template <class TIn, class TOut, int MODE>
+template <class TIn, class TOut, int MODE, bool ALIGNED, bool OUT_TILE, bool MASKS>
 cudaError_t launch_typed(const ShapeArgs& a, cudaStream_t st) {
-  const size_t smem = a.table ? static_cast<size_t>(a.cols) * 4 + a.cols / 8 : 0;
-  cudaError_t e = cudaFuncSetAttribute(shape_kernel<TIn, TOut, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       SH_MAX_COLS * 4 + SH_MAX_COLS / 8);
+  const auto bytes = [](size_t cols) {
+    return cols / 32 * 10 + SH_SET * 4 + SH_WARPS * (SH_STAGES + (OUT_TILE ? 1 : 0)) * SH_TILE;
+  };
+  const auto kernel = shape_kernel<TIn, TOut, MODE, ALIGNED, OUT_TILE, MASKS>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes(SH_MAX_COLS)));
   if (e != cudaSuccess) return e;
   const int64_t blocks = static_cast<int64_t>(a.ntiles) * ceil_div(a.R, a.rows_per_cta);
-  shape_kernel<TIn, TOut, MODE><<<static_cast<unsigned>(blocks), SH_THREADS, smem, st>>>(a);
+  kernel<<<static_cast<unsigned>(blocks), SH_THREADS, bytes(a.cols), st>>>(a);
   return cudaGetLastError();
+}
+
+template <class TIn, class TOut, int MODE>
+cudaError_t launch_vec(const ShapeArgs& a, cudaStream_t st) {
+  constexpr bool TILE = MODE != SHAPE_LOGP && sizeof(TIn) == sizeof(TOut);
+  const bool masks = a.s.allow_row != nullptr;
+  if (!a.vec_in || (TILE && !a.vec_out))  // the log-prob has no output rows, mixed types write theirs by element
+    return launch_typed<TIn, TOut, MODE, false, TILE, true>(a, st);
+  return masks ? launch_typed<TIn, TOut, MODE, true, false, true>(a, st) : launch_typed<TIn, TOut, MODE, true, false, false>(a, st);
 }
 
 template <int MODE>
@@ -486,20 +951,23 @@ cudaError_t launch_mode(const ShapeArgs& a, cudaStream_t st) {
   const bool in16 = a.dtype == GH_BF16, out16 = a.out_dtype == GH_BF16;
   if (MODE == SHAPE_OUT) {
     if (in16 != out16)
-      return in16 ? launch_typed<__nv_bfloat16, float, SHAPE_OUT>(a, st) : launch_typed<float, __nv_bfloat16, SHAPE_OUT>(a, st);
+      return in16 ? launch_vec<__nv_bfloat16, float, SHAPE_OUT>(a, st) : launch_vec<float, __nv_bfloat16, SHAPE_OUT>(a, st);
   }
-  return in16 ? launch_typed<__nv_bfloat16, __nv_bfloat16, MODE>(a, st) : launch_typed<float, float, MODE>(a, st);
+  return in16 ? launch_vec<__nv_bfloat16, __nv_bfloat16, MODE>(a, st) : launch_vec<float, float, MODE>(a, st);
 }
 
-// Columns and rows per CTA.
+// Columns and rows per CTA: as many columns as there are CTAs for two rounds of
+// the GPU, then as many rows as leave four.
 void plan(ShapeArgs& a) {
-  a.cols = SH_MAX_COLS;
-  while (a.cols > 4 * SH_SEG && static_cast<int64_t>(a.R) * ceil_div(a.V, a.cols) < 2 * num_sms()) a.cols /= 2;
+  const int64_t slots = static_cast<int64_t>(SH_CTAS) * num_sms();
+  int64_t tiles = ceil_div(a.V, SH_MAX_COLS);
+  const int64_t most = ceil_div(a.V, 4096);
+  while (tiles < most && a.R * tiles < 2 * slots) ++tiles;
+  a.cols = static_cast<int>(ceil_div(ceil_div(a.V, tiles), 1024) * 1024);
   a.ntiles = static_cast<int>(ceil_div(a.V, a.cols));
-  const int64_t rows = static_cast<int64_t>(a.R) * a.ntiles / (12 * num_sms());
+  const int64_t rows = static_cast<int64_t>(a.R) * a.ntiles / (4 * slots);
   a.rows_per_cta = static_cast<int>(rows < 1 ? 1 : (rows > SH_MAX_ROWS ? SH_MAX_ROWS : rows));
-  a.nseg = static_cast<int>(ceil_div(a.V, SH_SEG));
-  a.table = (a.s.hist_len || a.s.bias_set) ? 1 : 0;
+  a.nseg = static_cast<int>(ceil_div(a.V, a.dtype == GH_BF16 ? ShSeg<__nv_bfloat16>::COLS : ShSeg<float>::COLS));
   const size_t in_elt = a.dtype == GH_BF16 ? 2 : 4, out_elt = a.out_dtype == GH_BF16 ? 2 : 4;
   a.vec_in = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && a.ld * in_elt % 16 == 0;
   a.vec_out = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.out_ld * out_elt % 16 == 0;
@@ -507,7 +975,9 @@ void plan(ShapeArgs& a) {
 
 }  // namespace
 
-int64_t shape_segments(int64_t V) { return ceil_div(V, SH_SEG); }
+// an upper bound over the types: fp32 segments are the shorter ones
+int64_t shape_segments(int64_t V) { return ceil_div(V, SHAPE_MIN_SEG); }
+static_assert(SHAPE_MIN_SEG == ShSeg<float>::COLS && SHAPE_MIN_SEG <= ShSeg<__nv_bfloat16>::COLS, "workspace bound");
 
 cudaError_t launch_shape(ShapeArgs a, cudaStream_t st) {
   plan(a);

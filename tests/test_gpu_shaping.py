@@ -210,6 +210,18 @@ def test_history_lengths(gpu_lib, hist):
     _run_all(b, _values(rng, n, V, "bf16"), y, m, "bf16")
 
 
+def test_more_distinct_tokens_than_a_set_holds(gpu_lib):
+    # enough rows for wide column ranges, histories with thousands of distinct tokens in each of them
+    rng = np.random.default_rng(70)
+    n, V = 320, 33001
+    b = _batch(rng, n, V, hist=3)
+    b["tokens"] = np.concatenate([b["tokens"], rng.permutation(V)[:25000]]).astype(np.int32)
+    for i, k in ((3, 25000), (4, 25000), (5, 9000), (77, 24000), (319, 25000)):
+        b["hist_begin"][i], b["hist_len"][i], b["prompt_len"][i] = b["tokens"].size - k, k, k // 2
+    y, m = _targets(rng, n, V)
+    _run_all(b, _values(rng, n, V, "bf16"), y, m, "bf16")
+
+
 def test_training_sequence_grows_its_counts(gpu_lib):
     # enough rows that a CTA takes many consecutive ones: additions of one token, of several, rebuilds
     rng = np.random.default_rng(8)

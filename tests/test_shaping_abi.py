@@ -42,9 +42,9 @@ def _s(**kw):
 
 
 def test_workspace_size(lib):
-    # a (max, sum) pair per row and 1024 columns, and a target logit per row
+    # a (max, sum) pair per row and 512 columns, and a target logit per row
     al = lambda x: (x + 255) // 256 * 256  # noqa: E731
-    assert lib.grpo_shaped_logp_workspace_size(ctypes.byref(_s())) == al(10 * 3 * 8) + al(10 * 4)
+    assert lib.grpo_shaped_logp_workspace_size(ctypes.byref(_s())) == al(10 * 6 * 8) + al(10 * 4)
     assert lib.grpo_shaped_logp_workspace_size(ctypes.byref(_s(V=0))) == 0
 
 
