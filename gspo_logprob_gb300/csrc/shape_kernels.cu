@@ -47,8 +47,9 @@ namespace {
 constexpr int SH_THREADS = 256;
 constexpr int SH_WARPS = SH_THREADS / 32;
 constexpr int SH_CTAS = 4;                       // resident per SM: 32 warps of 64 registers a thread
-constexpr int SH_MAX_COLS = 32768;               // columns per CTA
+constexpr int SH_MAX_COLS = 38912;               // columns per CTA
 constexpr int SH_SET = 2048;                     // members the words have room for
+constexpr int SH_KEEP = 8;                       // history tokens a thread keeps while it builds a set
 constexpr int SH_MAX_ROWS = 32;                  // rows per CTA (one lane each in the set-up)
 constexpr float SH_LOG2E = 1.4426950408889634f;
 constexpr float SH_LOWEST = 3.402823466e38f;     // the largest finite fp32
@@ -338,16 +339,25 @@ __device__ int sh_build(const ShapeArgs& a, const ShSet& set, const ShRow& first
     for (int i = tid; i < nw; i += SH_THREADS) set.member[i] = 0;
     __syncthreads();
   }
+  // the first SH_KEEP tokens of each thread stay in registers for the counts: one latency for most histories
   const int32_t* h = a.s.tokens + last.begin;
-#pragma unroll 8
-  for (int k = tid; k < last.len; k += SH_THREADS) {
-    const uint32_t j = static_cast<uint32_t>(h[k] - c0);
-    if (j < static_cast<uint32_t>(cols)) atomicOr(&set.member[j >> 5], 1u << (j & 31));
+  uint32_t kept[SH_KEEP];
+  const int bk = last.bias_b + tid;
+  uint32_t bias_j = bk < last.bias_e ? static_cast<uint32_t>(a.s.bias_tokens[bk] - c0) : ~0u;
+#pragma unroll
+  for (int i = 0; i < SH_KEEP; ++i) {
+    const int k = tid + i * SH_THREADS;
+    kept[i] = k < last.len ? static_cast<uint32_t>(h[k] - c0) : ~0u;
   }
-  for (int k = last.bias_b + tid; k < last.bias_e; k += SH_THREADS) {
-    const uint32_t j = static_cast<uint32_t>(a.s.bias_tokens[k] - c0);
+  const auto mark = [&](uint32_t j) {
     if (j < static_cast<uint32_t>(cols)) atomicOr(&set.member[j >> 5], 1u << (j & 31));
-  }
+  };
+  mark(bias_j);
+#pragma unroll
+  for (int i = 0; i < SH_KEEP; ++i) mark(kept[i]);
+#pragma unroll 4
+  for (int k = tid + SH_KEEP * SH_THREADS; k < last.len; k += SH_THREADS) mark(static_cast<uint32_t>(h[k] - c0));
+  for (int k = bk + SH_THREADS; k < last.bias_e; k += SH_THREADS) mark(static_cast<uint32_t>(a.s.bias_tokens[k] - c0));
   __syncthreads();
   // ranks: each thread a run of words, then the runs before it
   const int run = (nw + SH_THREADS - 1) / SH_THREADS;
@@ -376,9 +386,9 @@ __device__ int sh_build(const ShapeArgs& a, const ShSet& set, const ShRow& first
   }
   for (int i = tid; i < total; i += SH_THREADS) set.word[i] = 0;
   __syncthreads();
-  if (first.bias_e > first.bias_b) {
-    for (int k = first.bias_b + tid; k < first.bias_e; k += SH_THREADS) {
-      const uint32_t j = static_cast<uint32_t>(a.s.bias_tokens[k] - c0);
+  if (first.bias_e > first.bias_b) {  // a chain has one list
+    for (int k = bk; k < first.bias_e; k += SH_THREADS) {
+      const uint32_t j = k == bk ? bias_j : static_cast<uint32_t>(a.s.bias_tokens[k] - c0);
       if (j < static_cast<uint32_t>(cols)) {
         // the last entry of a token counts
         atomicMax(&set.word[set.rank(j)], static_cast<uint32_t>(k - first.bias_b + 1) << SH_BIAS_SHIFT);
@@ -387,8 +397,13 @@ __device__ int sh_build(const ShapeArgs& a, const ShSet& set, const ShRow& first
     }
     __syncthreads();
   }
-#pragma unroll 8
-  for (int k = tid; k < first.len; k += SH_THREADS) {
+#pragma unroll
+  for (int i = 0; i < SH_KEEP; ++i) {
+    const int k = tid + i * SH_THREADS;
+    if (k < first.len && kept[i] < static_cast<uint32_t>(cols)) sh_count(set, kept[i], k < first.plen);
+  }
+#pragma unroll 4
+  for (int k = tid + SH_KEEP * SH_THREADS; k < first.len; k += SH_THREADS) {
     const uint32_t j = static_cast<uint32_t>(h[k] - c0);
     if (j < static_cast<uint32_t>(cols)) sh_count(set, j, k < first.plen);
   }
@@ -763,14 +778,16 @@ __global__ void __launch_bounds__(SH_THREADS, OUT_TILE ? 2 : SH_CTAS) shape_kern
                 acc[i & 1] = sh_add2(acc[i & 1], make_float2(ex2_approx(v.x), ex2_approx(v.y)));
               }
           } else {  // values near the type's lowest: the difference first
-#pragma unroll
-            for (int u = 0; u < S::CHUNKS; ++u)
+#pragma unroll 1
+            for (int u = 0; u < S::CHUNKS; ++u) {
+              sh_read<ShRaw<TIn>::N>(raw[0].w, buf + u * CB + lane * 16 * S::LANE16, shift);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const float2 v = sh_pair(raw[u], i);
+                const float2 v = sh_pair(raw[0], i);
                 acc[0].x += ex2_approx(fmaf(v.x, inv_t, -ref) * SH_LOG2E);
                 acc[0].y += ex2_approx(fmaf(v.y, inv_t, -ref) * SH_LOG2E);
               }
+            }
           }
           float sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
           if (sparse) sum += sl * ex2_approx((ml - ref) * SH_LOG2E);
@@ -956,18 +973,30 @@ cudaError_t launch_mode(const ShapeArgs& a, cudaStream_t st) {
   return in16 ? launch_vec<__nv_bfloat16, __nv_bfloat16, MODE>(a, st) : launch_vec<float, float, MODE>(a, st);
 }
 
-// Columns and rows per CTA: as many columns as there are CTAs for two rounds of
-// the GPU, then as many rows as leave four.
+// Columns and rows per CTA.  A round of the resident CTAs costs the segments of a
+// warp and about as much as four more for the rows' parameters and sets; the
+// number of column ranges with the least rounds times cost is taken.  256 rows of
+// 151936 columns: 4 ranges are 2 rounds and 54 us, 5 are 3 rounds and
+// 61 us.  Then as many rows per CTA as leave four rounds (chains get
+// longer; 8 rounds are within 1%).
 void plan(ShapeArgs& a) {
   const int64_t slots = static_cast<int64_t>(SH_CTAS) * num_sms();
-  int64_t tiles = ceil_div(a.V, SH_MAX_COLS);
-  const int64_t most = ceil_div(a.V, 4096);
-  while (tiles < most && a.R * tiles < 2 * slots) ++tiles;
-  a.cols = static_cast<int>(ceil_div(ceil_div(a.V, tiles), 1024) * 1024);
-  a.ntiles = static_cast<int>(ceil_div(a.V, a.cols));
+  const int seg = a.dtype == GH_BF16 ? ShSeg<__nv_bfloat16>::COLS : ShSeg<float>::COLS;
+  int64_t best = -1;
+  for (int64_t tiles = ceil_div(a.V, SH_MAX_COLS); tiles <= ceil_div(a.V, 4096); ++tiles) {
+    const int64_t cols = ceil_div(ceil_div(a.V, tiles), 1024) * 1024;
+    const int64_t n = ceil_div(a.V, cols);
+    const int64_t cost = ceil_div(a.R * n, slots) * (ceil_div(ceil_div(cols, seg), SH_WARPS) + 4);
+    if (best < 0 || cost < best) {
+      best = cost;
+      a.cols = static_cast<int>(cols);
+      a.ntiles = static_cast<int>(n);
+    }
+    if (tiles > 64 && a.R * tiles > 8 * slots) break;  // more ranges only add rounds
+  }
   const int64_t rows = static_cast<int64_t>(a.R) * a.ntiles / (4 * slots);
   a.rows_per_cta = static_cast<int>(rows < 1 ? 1 : (rows > SH_MAX_ROWS ? SH_MAX_ROWS : rows));
-  a.nseg = static_cast<int>(ceil_div(a.V, a.dtype == GH_BF16 ? ShSeg<__nv_bfloat16>::COLS : ShSeg<float>::COLS));
+  a.nseg = static_cast<int>(ceil_div(a.V, seg));
   const size_t in_elt = a.dtype == GH_BF16 ? 2 : 4, out_elt = a.out_dtype == GH_BF16 ? 2 : 4;
   a.vec_in = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && a.ld * in_elt % 16 == 0;
   a.vec_out = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.out_ld * out_elt % 16 == 0;
