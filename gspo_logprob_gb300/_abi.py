@@ -40,6 +40,12 @@ class GhGrpo(ctypes.Structure):
                 ("num_clipped", c_void_p)]
 
 
+class GhAdapter(ctypes.Structure):
+    _fields_ = [("N", c_int64), ("D", c_int64), ("V", c_int64), ("dtype", c_int32), ("out_dtype", c_int32),
+                ("rank", c_int32), ("num_adapters", c_int32), ("H", c_void_p), ("W", c_void_p), ("A", c_void_p),
+                ("B", c_void_p), ("scale", c_void_p), ("adapter_id", c_void_p), ("logits", c_void_p), ("ld", c_int64)]
+
+
 class GhShaping(ctypes.Structure):
     _fields_ = [("rows", c_int64), ("V", c_int64), ("tokens", c_void_p), ("num_tokens", c_int64),
                 ("hist_begin", c_void_p), ("hist_len", c_void_p), ("prompt_len", c_void_p), ("repetition", c_void_p),
@@ -82,6 +88,8 @@ SIGNATURES = {
     "grpo_dh_merge": (c_int32, [c_int32, c_int64, c_int64, c_int32, c_void_p, c_void_p, c_void_p, c_void_p]),
     "grpo_loss_from_sequence_totals": (c_int32, [c_int32, c_void_p, c_void_p, c_void_p, c_int32, c_double, c_float,
                                                  c_void_p, c_void_p, c_void_p]),
+    "grpo_adapter_logits_workspace_size": (c_size_t, [POINTER(GhAdapter)]),
+    "grpo_adapter_logits": (c_int32, [POINTER(GhAdapter), c_void_p, c_void_p, c_size_t, c_void_p]),
     "grpo_shape_logits": (c_int32, [POINTER(GhShaping), c_void_p, c_int32, c_int64, c_void_p, c_int32, c_int64,
                                     c_void_p, c_void_p]),
     "grpo_shaped_logp_workspace_size": (c_size_t, [POINTER(GhShaping)]),

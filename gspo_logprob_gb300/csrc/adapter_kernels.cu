@@ -1,0 +1,750 @@
+// Logits of a shared head with low-rank adapters, one per row:
+//   z_i = W h_i + s_a B_a (A_a h_i),   a = adapter_id[i] (or none).
+//
+// bf16: two launches.  The first forms u_i = s_a A_a h_i (fp32 sums) and lays it
+// out for the tensor cores; the second is one tcgen05 product whose K runs over
+// the hidden size and then over 16-wide chunks of the adapters in use:
+//   Z = H W^T + sum_a U_a B_a^T,   U_a = u_i in the rows of adapter a, else 0.
+// The rows of a tile need not be sorted by adapter, the low-rank part costs a
+// pass over the B_a in use and nothing is added to the logits afterwards.  Decode
+// batches are bound by the read of W (a row tile of requests multiplies every W
+// tile once), prompts by the tensor cores; a chunk is two MMAs of K = 16.
+// u is given as two bf16 terms, high and low, each its own MMA on the same B
+// chunk: one term alone would round u to 8 bits (an error of 2^-9 of the
+// adapter's part, visible in fp32 logits), both leave 2^-17, at 4 KB more
+// shared-memory traffic per chunk.
+//
+// fp32: exact fp32 FMA, no TF32, as the rest of the head.
+#include <cuda_bf16.h>
+
+#include <mutex>
+
+#include "internal.h"
+#include "tc_gemm.cuh"
+#include "tc_gemm_pair.cuh"
+
+namespace gh {
+namespace {
+
+// ---------------------------------------------------------------- u = s A h
+constexpr int AD_THREADS = 256;
+constexpr int AD_RANKS = 8;  // ranks per CTA: one per warp
+
+// One CTA: RPC consecutive rows (of one row tile) times 8 ranks.  It finds the
+// adapters of the row tile in the order of their first rows (the tile's slots),
+// and writes its rows' part of every slot's chunk: u in their own slot, 0 in the
+// others.  U: [tiles, max_chunks, high/low, tile rows, 16] bf16; list: per tile
+// the number of slots, then each slot's adapter.
+// RPC = 1 for decode (latency: one dot per warp), 8 for prompts (a row of A_a is
+// read once for eight rows of the same request).
+template <int RPC>
+__global__ void __launch_bounds__(AD_THREADS) adapter_low_kernel(const AdapterArgs a) {
+  __shared__ int ids[256];
+  __shared__ int first[256];  // first row of the tile with the same adapter
+  __shared__ int slot_of[256];
+  __shared__ int warp_n[AD_THREADS / 32];
+  __shared__ float u[RPC][AD_RANKS];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int row0 = blockIdx.x * RPC;
+  const int tile = row0 / a.tile_rows, base = tile * a.tile_rows;
+  const int j = blockIdx.y * AD_RANKS + warp;
+
+  int id = -1;
+  if (tid < a.tile_rows && base + tid < a.N) {
+    id = a.ids[base + tid];
+    if (id < -1 || id >= a.num_adapters) {
+      if (row0 == base && blockIdx.y == 0) atomicOr(a.status, GH_DEV_BAD_ROW);
+      id = -1;
+    }
+  }
+  ids[tid] = id;
+  __syncthreads();
+  // the dot products need the rows' adapters only
+  float acc[RPC];
+#pragma unroll
+  for (int q = 0; q < RPC; ++q) acc[q] = 0.f;
+  if (j < a.rank) {
+    int rid[RPC];
+    bool any = false;
+#pragma unroll
+    for (int q = 0; q < RPC; ++q) {
+      rid[q] = ids[row0 - base + q];
+      any |= rid[q] >= 0;
+    }
+    if (any) {
+      const size_t astep = static_cast<size_t>(a.rank) * a.D;
+      const __nv_bfloat16* A0 = static_cast<const __nv_bfloat16*>(a.A) + static_cast<size_t>(j) * a.D;
+      const __nv_bfloat16* H0 = static_cast<const __nv_bfloat16*>(a.H) + static_cast<size_t>(row0) * a.D;
+#pragma unroll 4
+      for (int k = lane * 8; k < a.D; k += 256) {
+        float w[8];
+#pragma unroll
+        for (int q = 0; q < RPC; ++q) {
+          if (rid[q] < 0) continue;
+          if (q == 0 || rid[q] != rid[q - 1]) {
+            const uint4 t = __ldg(reinterpret_cast<const uint4*>(A0 + rid[q] * astep + k));
+            const uint32_t tw[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              w[2 * i] = __uint_as_float(tw[i] << 16);
+              w[2 * i + 1] = __uint_as_float(tw[i] & 0xffff0000u);
+            }
+          }
+          const uint4 t = __ldg(reinterpret_cast<const uint4*>(H0 + static_cast<size_t>(q) * a.D + k));
+          const uint32_t hw[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            acc[q] = fmaf(w[2 * i], __uint_as_float(hw[i] << 16), acc[q]);
+            acc[q] = fmaf(w[2 * i + 1], __uint_as_float(hw[i] & 0xffff0000u), acc[q]);
+          }
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < RPC; ++q) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) acc[q] += __shfl_xor_sync(0xffffffffu, acc[q], o);
+      }
+    }
+    if (lane == 0) {
+#pragma unroll
+      for (int q = 0; q < RPC; ++q) u[q][warp] = rid[q] < 0 ? 0.f : acc[q] * a.scale[rid[q]];
+    }
+  } else if (lane == 0) {
+#pragma unroll
+    for (int q = 0; q < RPC; ++q) u[q][warp] = 0.f;
+  }
+  // slots
+  int f = tid;
+  if (id >= 0) {
+    for (int t = 0; t < tid; ++t)
+      if (ids[t] == id) {
+        f = t;
+        break;
+      }
+  }
+  const bool lead = id >= 0 && f == tid;
+  first[tid] = f;
+  const uint32_t leads = __ballot_sync(0xffffffffu, lead);
+  if (lane == 0) warp_n[warp] = __popc(leads);
+  __syncthreads();
+  int off = 0, slots = 0;
+  for (int w = 0; w < AD_THREADS / 32; ++w) {
+    if (w < warp) off += warp_n[w];
+    slots += warp_n[w];
+  }
+  off += __popc(leads & ((1u << lane) - 1u));
+  slot_of[tid] = off;
+  if (lead && row0 == base && blockIdx.y == 0) a.list[static_cast<size_t>(tile) * a.list_ld + 1 + off] = id;
+  if (tid == 0 && row0 == base && blockIdx.y == 0) a.list[static_cast<size_t>(tile) * a.list_ld] = slots;
+  __syncthreads();
+  // this CTA's half (8 ranks) of one chunk of every slot
+  const int rc = a.rank_chunks, chunk = blockIdx.y >> 1, half = blockIdx.y & 1;
+  uint4* U = static_cast<uint4*>(a.U);
+  for (int i = tid; i < slots * RPC * 2; i += AD_THREADS) {
+    const int hl = i & 1, q = (i >> 1) % RPC, s = (i >> 1) / RPC;
+    const int row = row0 + q - base;
+    if (base + row >= a.N) continue;
+    uint32_t w[4] = {0, 0, 0, 0};
+    if (ids[row] >= 0 && slot_of[first[row]] == s) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float x = u[q][2 * e], y = u[q][2 * e + 1];
+        if (hl) {  // what the rounding to the high term left
+          x -= __bfloat162float(__float2bfloat16_rn(x));
+          y -= __bfloat162float(__float2bfloat16_rn(y));
+        }
+        const __nv_bfloat162 p = __floats2bfloat162_rn(x, y);
+        w[e] = *reinterpret_cast<const uint32_t*>(&p);
+      }
+    }
+    const size_t at =
+        ((static_cast<size_t>(tile) * a.max_chunks + (s * rc + chunk)) * 2 + hl) * a.tile_rows + row;
+    U[at * 2 + half] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// ---------------------------------------------------------------- Z = [H U] [W B]^T
+// Shared-memory descriptor of a K-major tile of 16 bf16 (32-byte rows, 32-byte
+// swizzle: 8-row groups at 256 bytes).
+__device__ __forceinline__ uint64_t sdesc_sw32(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(1u) << 16;
+  d |= static_cast<uint64_t>(256u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(6u) << 61;
+  return d;
+}
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// PAIR = false: a CTA computes 128 rows by bn columns (up to 256): decode, where
+// every CTA streams its own W tiles.  PAIR = true: two CTAs share a 256 x 256 tile
+// (cta_group::2), each staging its 128 rows of H and its half of the W tile:
+// prompts, where the operands' L2 traffic per FLOP counts.
+template <bool PAIR>
+struct AdCfg {
+  static constexpr int A_BYTES = TC_BM * TC_BK * 2;
+  static constexpr int B_ROWS = PAIR ? TC_BN / 2 : TC_BN;
+  static constexpr int STAGE_BYTES = A_BYTES + B_ROWS * TC_BK * 2;
+  static constexpr int STAGES = PAIR ? 6 : 4;  // 192 KB in flight per SM
+  static constexpr int U_BYTES = TC_BM * 32;   // one term of a chunk
+  static constexpr int CHUNK_BYTES = 2 * U_BYTES + B_ROWS * 32;
+  static constexpr int CHUNKS = 2;  // low-rank chunks per stage
+  static constexpr int EPI_WARPS = 4;
+  static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+  static constexpr int TURN_LD = 33;  // fp32 transpose tile of an epilogue warp
+  static constexpr int TURN_BYTES = 32 * TURN_LD * 4;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_WARPS * TURN_BYTES + 1024 + 256;
+  static_assert(CHUNKS * CHUNK_BYTES <= STAGE_BYTES, "chunks share the stages");
+};
+
+// 32 columns of a row per thread to the output; rows of a warp are consecutive.
+template <class TOut>
+__device__ __forceinline__ void ad_store(const AdapterArgs& a, const float* v, int row, int col0, int lane, float* turn) {
+  const int cols = min(32, a.V - col0);
+  TOut* out = static_cast<TOut*>(a.out);
+  if (a.vec_out && cols == 32) {
+    if (row < a.N) {
+      uint4* d = reinterpret_cast<uint4*>(out + static_cast<size_t>(row) * a.ld + col0);
+      if constexpr (sizeof(TOut) == 2) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[8 * q + 2 * i], v[8 * q + 2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          d[q] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          d[q] = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
+                            __float_as_uint(v[4 * q + 3]));
+      }
+    }
+    return;
+  }
+  // rows that do not start on 16 bytes: turned over, so that a row's 32 columns are stored side by side
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) turn[lane * 33 + i] = v[i];
+  __syncwarp();
+  const int row_w = row - lane;
+  if (lane < cols) {
+    const int n = min(32, a.N - row_w);
+    for (int i = 0; i < n; ++i) {
+      TOut* d = out + static_cast<size_t>(row_w + i) * a.ld + col0 + lane;
+      if constexpr (sizeof(TOut) == 2)
+        *d = __float2bfloat16_rn(turn[i * 33 + lane]);
+      else
+        *d = turn[i * 33 + lane];
+    }
+  }
+}
+
+template <bool PAIR, class TOut>
+__global__ void __launch_bounds__(AdCfg<PAIR>::THREADS, 1)
+    adapter_tc_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CUtensorMap tmW,
+                      const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmB, const TcSched sc,
+                      const int bn, const AdapterArgs a, const uint64_t timeout_ns) {
+  using C = AdCfg<PAIR>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* turn_all = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE_BYTES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::STAGE_BYTES + C::EPI_WARPS * C::TURN_BYTES);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* tfull = empty + C::STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0;  // the even CTA of a pair issues its MMAs
+  const int cid = PAIR ? blockIdx.x >> 1 : blockIdx.x, ncl = PAIR ? gridDim.x >> 1 : gridDim.x;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], (PAIR ? 2 : 1) * C::EPI_WARPS);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();
+    prefetch_tmap(&tmH);
+    prefetch_tmap(&tmW);
+    prefetch_tmap(&tmU);
+    prefetch_tmap(&tmB);
+  }
+  if (warp == 1) {
+    if (PAIR) {
+      tmem_alloc_pair(tmem_slot, TC_TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, TC_TMEM_COLS);
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before();
+  if (PAIR)
+    cluster_sync_all();
+  else
+    __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int rc = a.rank_chunks;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------ TMA producer (both CTAs of a pair)
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t pending = 0, pend_par = 0;  // per stage: load issued and its phase parity
+      bool ok = true, issued = false;
+      const auto open_stage = [&](uint32_t bytes) {
+        if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, a.status, GH_DEV_TIMEOUT, timeout_ns)) {
+          ok = false;
+          return false;
+        }
+        if (PAIR) {
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * bytes);
+        } else {
+          mbar_arrive_expect_tx(&full[stage], bytes);
+        }
+        return true;
+      };
+      const auto load2 = [&](uint8_t* dst, const CUtensorMap* map, int c0, int c1) {
+        if (PAIR)
+          tma_load_2d_pair(dst, map, mapa_shared(smem_u32(&full[stage]), 0), c0, c1);
+        else
+          tma_load_2d(dst, map, &full[stage], c0, c1);
+      };
+      const auto load3 = [&](uint8_t* dst, const CUtensorMap* map, int c0, int c1, int c2) {
+        if (PAIR)
+          tma_load_3d_pair(dst, map, mapa_shared(smem_u32(&full[stage]), 0), c0, c1, c2);
+        else
+          tma_load_3d(dst, map, &full[stage], c0, c1, c2);
+      };
+      const auto close_stage = [&] {
+        issued = true;
+        pending |= 1u << stage;
+        pend_par = (pend_par & ~(1u << stage)) | (phase << stage);
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      };
+      for (int task = cid; ok && task < sc.num_tasks; task += ncl) {
+        int m_blk, n_blk;
+        tc_task_of(sc, task, m_blk, n_blk);
+        const int m0 = m_blk * sc.m_step + static_cast<int>(rank) * TC_BM;
+        const int n0 = n_blk * bn + static_cast<int>(rank) * (TC_BN / 2);
+        const int b_rows = PAIR ? C::B_ROWS : bn;
+        for (int kb = 0; kb < sc.num_kb; ++kb) {
+          if (!open_stage(C::A_BYTES + b_rows * TC_BK * 2)) break;
+          uint8_t* s = smem + stage * C::STAGE_BYTES;
+          load2(s, &tmH, kb * TC_BK, m0);
+          load2(s + C::A_BYTES, &tmW, kb * TC_BK, n0);
+          close_stage();
+        }
+        const int* list = a.list + static_cast<size_t>(m_blk) * a.list_ld;
+        const int chunks = ok ? list[0] * rc : 0;
+        for (int c0 = 0; ok && c0 < chunks; c0 += C::CHUNKS) {
+          const int n = min(C::CHUNKS, chunks - c0);
+          if (!open_stage(n * (2 * C::U_BYTES + b_rows * 32))) break;
+          for (int q = 0; q < n; ++q) {
+            uint8_t* s = smem + stage * C::STAGE_BYTES + q * C::CHUNK_BYTES;
+            const int c = c0 + q;
+            const int u0 = ((m_blk * a.max_chunks + c) * 2) * a.tile_rows + static_cast<int>(rank) * TC_BM;
+            load3(s, &tmU, 0, u0, 0);
+            load3(s + C::U_BYTES, &tmU, 0, u0 + a.tile_rows, 0);
+            load3(s + 2 * C::U_BYTES, &tmB, (c % rc) * 16, n0, list[1 + c / rc]);
+          }
+          close_stage();
+        }
+      }
+      if (!ok) {
+        if (PAIR) {
+          // completions land on the even CTA's barriers, which this CTA cannot
+          // poll: give copies in flight a fixed, bounded time to land
+          const uint64_t t0 = globaltimer_ns();
+          while (issued && globaltimer_ns() - t0 < 2000000ull) {
+          }
+        } else {
+          for (int s = 0; s < C::STAGES; ++s)
+            if (pending & (1u << s)) {
+              volatile int no_abort = 0;
+              mbar_wait_bounded(&full[s], (pend_par >> s) & 1u, &no_abort, nullptr, 0, timeout_ns);
+            }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      // ------------------------------------------------ MMA issuer
+      const uint32_t idesc = PAIR ? idesc_bf16_f32(2 * TC_BM, TC_BN, false, false) : idesc_bf16_f32(TC_BM, bn, false, false);
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool ok = true, issued = false;
+      const auto wait_stage = [&] {
+        if (!mbar_wait_bounded(&full[stage], phase, abort_flag, a.status, GH_DEV_TIMEOUT, timeout_ns)) {
+          ok = false;
+          return false;
+        }
+        tc_fence_after();
+        return true;
+      };
+      const auto mma = [&](uint32_t d, uint64_t ad, uint64_t bd, uint32_t add) {
+        if (PAIR)
+          umma_pair_bf16(d, ad, bd, idesc, add);
+        else
+          umma_bf16(d, ad, bd, idesc, add);
+      };
+      const auto free_stage = [&] {
+        issued = true;
+        if (PAIR)
+          umma_pair_commit_mc(&empty[stage], 0x3);
+        else
+          umma_commit(&empty[stage]);
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      };
+      for (int task = cid; ok && task < sc.num_tasks; task += ncl) {
+        int m_blk, n_blk;
+        tc_task_of(sc, task, m_blk, n_blk);
+        if (!mbar_wait_bounded(&tempty[acc], acc_phase ^ 1u, abort_flag, a.status, GH_DEV_TIMEOUT, timeout_ns)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem_base + static_cast<uint32_t>(acc * TC_BN);
+        for (int kb = 0; kb < sc.num_kb; ++kb) {
+          if (!wait_stage()) break;
+          const uint32_t ab = smem_u32(smem + stage * C::STAGE_BYTES), bb = ab + C::A_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < TC_BK / 16; ++kk)
+            mma(d, sdesc_sw128(ab + kk * 32, 16, 1024), sdesc_sw128(bb + kk * 32, 16, 1024), (kb | kk) != 0 ? 1u : 0u);
+          free_stage();
+        }
+        const int chunks = ok ? a.list[static_cast<size_t>(m_blk) * a.list_ld] * rc : 0;
+        for (int c0 = 0; ok && c0 < chunks; c0 += C::CHUNKS) {
+          if (!wait_stage()) break;
+          const int n = min(C::CHUNKS, chunks - c0);
+          for (int q = 0; q < n; ++q) {
+            const uint32_t ub = smem_u32(smem + stage * C::STAGE_BYTES + q * C::CHUNK_BYTES);
+            const uint64_t bd = sdesc_sw32(ub + 2 * C::U_BYTES);
+            mma(d, sdesc_sw32(ub), bd, 1u);
+            mma(d, sdesc_sw32(ub + C::U_BYTES), bd, 1u);
+          }
+          free_stage();
+        }
+        if (!ok) break;
+        if (PAIR)
+          umma_pair_commit_mc(&tfull[acc], 0x3);
+        else
+          umma_commit(&tfull[acc]);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      if (issued) {
+        // every MMA issued must be complete before TMEM is freed
+        if (PAIR)
+          umma_pair_commit_mc(drain, 0x1);
+        else
+          umma_commit(drain);
+        volatile int no_abort = 0;
+        mbar_wait_bounded(drain, 0, &no_abort, nullptr, 0, timeout_ns);
+      }
+    }
+  } else {
+    // -------------------------------------------------- epilogue warps (both CTAs)
+    const int sub = warp & 3;  // TMEM lane quarter this warp may access
+    const uint32_t lane_addr = static_cast<uint32_t>(sub * 32) << 16;
+    float* turn = turn_all + (warp - 2) * (C::TURN_BYTES / 4);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int task = cid; task < sc.num_tasks; task += ncl) {
+      int m_blk, n_blk;
+      tc_task_of(sc, task, m_blk, n_blk);
+      if (!warp_wait(&tfull[acc], acc_phase, abort_flag, a.status, timeout_ns)) break;
+      tc_fence_after();
+      const int row = m_blk * sc.m_step + static_cast<int>(rank) * TC_BM + sub * 32 + lane;
+      if (row - lane < a.N) {
+#pragma unroll 1
+        for (int c = 0; c < bn / 32; ++c) {
+          const int col0 = n_blk * bn + c * 32;
+          if (col0 >= a.V) break;
+          float v[32];
+          tmem_ld32(tmem_base + lane_addr + static_cast<uint32_t>(acc * TC_BN + c * 32), v);
+          ad_store<TOut>(a, v, row, col0, lane, turn);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (!PAIR || rank == 0)
+          mbar_arrive(&tempty[acc]);
+        else
+          mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
+      }
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  if (PAIR)
+    cluster_sync_all();
+  else
+    __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    if (PAIR)
+      tmem_dealloc_pair(tmem_base, TC_TMEM_COLS);
+    else
+      tmem_dealloc(tmem_base, TC_TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------- fp32
+// u [N, rank] = s_a A_a h_i: a warp per (row, rank).
+__global__ void __launch_bounds__(256) adapter_low_f32_kernel(const AdapterArgs a) {
+  const long long w = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (w >= static_cast<long long>(a.N) * a.rank) return;
+  const int row = static_cast<int>(w / a.rank), j = static_cast<int>(w % a.rank);
+  const int id = a.ids[row];
+  float* u = static_cast<float*>(a.U) + w;
+  if (id < 0 || id >= a.num_adapters) {
+    if (lane == 0) {
+      *u = 0.f;
+      if (id != -1) atomicOr(a.status, GH_DEV_BAD_ROW);
+    }
+    return;
+  }
+  const float* A = static_cast<const float*>(a.A) + (static_cast<size_t>(id) * a.rank + j) * a.D;
+  const float* h = static_cast<const float*>(a.H) + static_cast<size_t>(row) * a.D;
+  float s = 0.f;
+  for (int k = lane; k < a.D; k += 32) s = fmaf(A[k], h[k], s);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0) *u = s * a.scale[id];
+}
+
+// 64 x 64 logits per CTA, 4 x 4 per thread, both operands K-contiguous and turned
+// over in shared memory; then each row's low-rank part, u_i . B_a[v], added.
+constexpr int F32_T = 64, F32_K = 16;
+__global__ void __launch_bounds__(256) adapter_f32_kernel(const AdapterArgs a) {
+  __shared__ __align__(16) float Hs[F32_K][F32_T + 4];
+  __shared__ __align__(16) float Ws[F32_K][F32_T + 4];
+  const int t = threadIdx.x, tr = t / 16, tc = t % 16;
+  const int m0 = blockIdx.y * F32_T, n0 = blockIdx.x * F32_T;
+  const float* H = static_cast<const float*>(a.H);
+  const float* W = static_cast<const float*>(a.W);
+  float acc[4][4] = {};
+  for (int k0 = 0; k0 < a.D; k0 += F32_K) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int e = t + 256 * q, r = e / F32_K, k = e % F32_K;
+      const bool in = k0 + k < a.D;
+      Hs[k][r] = in && m0 + r < a.N ? H[static_cast<size_t>(m0 + r) * a.D + k0 + k] : 0.f;
+      Ws[k][r] = in && n0 + r < a.V ? W[static_cast<size_t>(n0 + r) * a.D + k0 + k] : 0.f;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < F32_K; ++k) {
+      const float4 x = *reinterpret_cast<const float4*>(&Hs[k][4 * tr]);
+      const float4 y = *reinterpret_cast<const float4*>(&Ws[k][4 * tc]);
+      const float xv[4] = {x.x, x.y, x.z, x.w}, yv[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xv[i], yv[j], acc[i][j]);
+    }
+    __syncthreads();
+  }
+  const float* U = static_cast<const float*>(a.U);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = m0 + 4 * tr + i;
+    if (row >= a.N) continue;
+    const int id = a.ids[row];
+    const bool on = id >= 0 && id < a.num_adapters;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int v = n0 + 4 * tc + j;
+      if (v >= a.V) continue;
+      float s = 0.f;
+      if (on) {
+        const float* B = static_cast<const float*>(a.B) + (static_cast<size_t>(id) * a.V + v) * a.rank;
+        for (int k = 0; k < a.rank; ++k) s = fmaf(U[static_cast<size_t>(row) * a.rank + k], B[k], s);
+      }
+      static_cast<float*>(a.out)[static_cast<size_t>(row) * a.ld + v] = on ? acc[i][j] + s : acc[i][j];
+    }
+  }
+}
+
+// columns per tile of the single-CTA form: the widest of those that cost the
+// fewest columns in the longest CTA (a tile re-reads the rows of H, half as dear)
+int decode_cols(int N, int V) {
+  int best = 256;
+  int64_t cost = -1;
+  for (int bn = 256; bn >= 32; bn -= 32) {
+    const int64_t c = ceil_div(ceil_div(V, bn), num_sms()) * (2 * bn + (N < TC_BM ? N : TC_BM));
+    if (cost < 0 || c < cost) {
+      cost = c;
+      best = bn;
+    }
+  }
+  return best;
+}
+
+struct AdSetup {
+  std::mutex mu;
+  bool done[64] = {};
+  int pairs[64] = {};
+};
+
+template <bool PAIR, class TOut>
+cudaError_t launch_product(const AdapterArgs& a, cudaStream_t st) {
+  using C = AdCfg<PAIR>;
+  auto kern = adapter_tc_kernel<PAIR, TOut>;
+  static AdSetup setup;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) dev = 0;
+  int pairs_fit;
+  {
+    std::lock_guard<std::mutex> g(setup.mu);
+    if (!setup.done[dev]) {
+      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+      if (e != cudaSuccess) return e;
+      int n = num_sms() / 2;
+      if (PAIR) {
+        cudaLaunchConfig_t q = {};
+        q.gridDim = dim3(2 * n);
+        q.blockDim = dim3(C::THREADS);
+        q.dynamicSmemBytes = C::SMEM_BYTES;
+        cudaLaunchAttribute qa[1];
+        qa[0].id = cudaLaunchAttributeClusterDimension;
+        qa[0].val.clusterDim.x = 2;
+        qa[0].val.clusterDim.y = 1;
+        qa[0].val.clusterDim.z = 1;
+        q.attrs = qa;
+        q.numAttrs = 1;
+        int fit = 0;
+        if (cudaOccupancyMaxActiveClusters(&fit, kern, &q) == cudaSuccess && fit > 0 && fit < n) n = fit;
+        (void)cudaGetLastError();
+      }
+      setup.pairs[dev] = n > 0 ? n : 1;
+      setup.done[dev] = true;
+    }
+    pairs_fit = setup.pairs[dev];
+  }
+  const int bn = PAIR ? TC_BN : decode_cols(a.N, a.V);
+  const uint32_t b_rows = PAIR ? C::B_ROWS : bn;
+  CUtensorMap th, tw, tu, tb;
+  const uint64_t row_bytes = static_cast<uint64_t>(a.D) * 2;
+  const int tiles = static_cast<int>(ceil_div(a.N, a.tile_rows));
+  const uint64_t u_rows = static_cast<uint64_t>(tiles) * a.max_chunks * 2 * a.tile_rows;
+  if (!make_tmap_bf16(&th, a.H, a.D, a.N, row_bytes, TC_BK, TC_BM) ||
+      !make_tmap_bf16(&tw, a.W, a.D, a.V, row_bytes, TC_BK, b_rows) ||
+      !make_tmap_bf16_k16(&tu, a.U, 16, u_rows, 1, 32, u_rows * 32, TC_BM) ||
+      !make_tmap_bf16_k16(&tb, a.B, a.rank, a.V, a.num_adapters, static_cast<uint64_t>(a.rank) * 2,
+                          static_cast<uint64_t>(a.V) * a.rank * 2, b_rows))
+    return cudaErrorInvalidValue;
+  TcSched sc;
+  sc.num_m_blocks = tiles;
+  sc.num_n_blocks = static_cast<int>(ceil_div(a.V, bn));
+  sc.n_per_task = 1;
+  sc.num_kb = static_cast<int>(ceil_div(a.D, TC_BK));
+  sc.m_step = a.tile_rows;
+  sc.group_m = tiles < 16 ? tiles : 16;  // the head forward's raster: a group's rows stay in L2 while W streams past
+  sc.num_ng = sc.num_n_blocks;
+  sc.num_tasks = sc.num_m_blocks * sc.num_ng;
+  cudaLaunchConfig_t cfg = {};
+  const int most = PAIR ? pairs_fit : num_sms();
+  const int n = sc.num_tasks < most ? sc.num_tasks : most;
+  cfg.gridDim = dim3(PAIR ? 2 * n : n);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 1 : 0;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, th, tw, tu, tb, sc, bn, a, timeout_ns());
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// Rows up to one single-CTA tile (128) take that form; more take pairs.
+AdapterPlan adapter_plan(int64_t N, int64_t rank, int64_t num_adapters) {
+  AdapterPlan p;
+  p.tile_rows = N <= TC_BM ? TC_BM : 2 * TC_BM;
+  p.rank_chunks = static_cast<int>(ceil_div(rank, 16));
+  const int64_t slots = num_adapters < p.tile_rows ? num_adapters : p.tile_rows;
+  p.max_chunks = static_cast<int>(slots * p.rank_chunks);
+  p.list_ld = 1 + static_cast<int>(slots);
+  const int64_t tiles = ceil_div(N, p.tile_rows);
+  p.u_rows = tiles * p.max_chunks * 2 * p.tile_rows;
+  p.u_bytes = align_up(static_cast<size_t>(p.u_rows) * 32, 256);
+  p.list_bytes = align_up(static_cast<size_t>(tiles) * p.list_ld * 4, 256);
+  return p;
+}
+
+cudaError_t launch_adapter_low(const AdapterArgs& a, cudaStream_t st) {
+  if (a.dtype == GH_FP32) {
+    const int64_t warps = static_cast<int64_t>(a.N) * a.rank;
+    adapter_low_f32_kernel<<<static_cast<unsigned>(ceil_div(warps, 8)), 256, 0, st>>>(a);
+  } else {
+    const unsigned y = static_cast<unsigned>(2 * a.rank_chunks);
+    if (a.N < 1024)
+      adapter_low_kernel<1><<<dim3(a.N, y), AD_THREADS, 0, st>>>(a);
+    else
+      adapter_low_kernel<8><<<dim3(static_cast<unsigned>(ceil_div(a.N, 8)), y), AD_THREADS, 0, st>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_adapter_logits(const AdapterArgs& a, cudaStream_t st) {
+  if (a.dtype == GH_FP32) {
+    const dim3 grid(static_cast<unsigned>(ceil_div(a.V, F32_T)), static_cast<unsigned>(ceil_div(a.N, F32_T)));
+    adapter_f32_kernel<<<grid, 256, 0, st>>>(a);
+    return cudaGetLastError();
+  }
+  if (a.tile_rows == TC_BM)
+    return a.out_dtype == GH_BF16 ? launch_product<false, __nv_bfloat16>(a, st) : launch_product<false, float>(a, st);
+  return a.out_dtype == GH_BF16 ? launch_product<true, __nv_bfloat16>(a, st) : launch_product<true, float>(a, st);
+}
+
+}  // namespace gh

@@ -114,6 +114,20 @@ bool make_tmap_bf16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t
   return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_bf16_k16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint64_t depth,
+                        uint64_t row_stride, uint64_t depth_stride, uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {inner, rows, depth};
+  cuuint64_t strides[2] = {row_stride, depth_stride};
+  cuuint32_t box[3] = {16, box_rows, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // ---------------------------------------------------------------- instrumentation
 struct Prof {
   bool on = false;
@@ -916,6 +930,96 @@ gh_status grpo_shaped_logp_backward(const gh_shaping* shaping, const void* logit
   return GH_OK;
 }
 
+// ---------------------------------------------------------------- head with adapters
+static gh_status check_adapter(const gh_adapter* p) {
+  if (!p) return fail(GH_ERR_INVALID_ARG, "adapter problem is NULL");
+  if (p->N < 0 || p->N > (int64_t(1) << 24)) return fail(GH_ERR_INVALID_ARG, "N=%lld out of range", (long long)p->N);
+  if (p->D < 1 || p->D > (int64_t(1) << 20)) return fail(GH_ERR_INVALID_ARG, "D=%lld out of range", (long long)p->D);
+  if (p->V < 1 || p->V > (int64_t(1) << 28)) return fail(GH_ERR_INVALID_ARG, "V=%lld out of range", (long long)p->V);
+  if (p->dtype != GH_BF16 && p->dtype != GH_FP32) return fail(GH_ERR_INVALID_ARG, "dtype=%d unknown", p->dtype);
+  if (p->out_dtype != GH_BF16 && p->out_dtype != GH_FP32)
+    return fail(GH_ERR_INVALID_ARG, "out_dtype=%d unknown", p->out_dtype);
+  if (p->dtype == GH_FP32 && p->out_dtype != GH_FP32) return fail(GH_ERR_INVALID_ARG, "fp32 heads give fp32 logits");
+  if (p->rank < 1 || p->rank > 256) return fail(GH_ERR_INVALID_ARG, "rank=%d out of [1, 256]", p->rank);
+  if (p->num_adapters < 1 || p->num_adapters > 65535)
+    return fail(GH_ERR_INVALID_ARG, "num_adapters=%d out of [1, 65535]", p->num_adapters);
+  if (p->dtype == GH_BF16) {
+    if (p->D % 8 != 0 || p->rank % 8 != 0)
+      return fail(GH_ERR_INVALID_ARG, "bf16 needs D %% 8 == 0 and rank %% 8 == 0 (D=%lld, rank=%d)", (long long)p->D,
+                  p->rank);
+    if (adapter_plan(p->N, p->rank, p->num_adapters).u_rows > INT32_MAX)
+      return fail(GH_ERR_INVALID_ARG, "N x adapters x rank is too large for one call: split the rows");
+  } else if (ceil_div(p->N, 64) > 65535 || p->N * p->rank > INT32_MAX) {
+    return fail(GH_ERR_INVALID_ARG, "N=%lld is too large for one fp32 call: split the rows", (long long)p->N);
+  }
+  if (ceil_div(p->N, 128) * ceil_div(p->V, 32) > INT32_MAX)
+    return fail(GH_ERR_INVALID_ARG, "N x V is too large for one call: split the rows");
+  return GH_OK;
+}
+
+size_t grpo_adapter_logits_workspace_size(const gh_adapter* p) {
+  if (check_adapter(p) != GH_OK) return 0;
+  if (p->dtype == GH_FP32) return align_up(static_cast<size_t>(p->N) * p->rank * 4, 256);
+  const AdapterPlan q = adapter_plan(p->N, p->rank, p->num_adapters);
+  return q.u_bytes + q.list_bytes;
+}
+
+gh_status grpo_adapter_logits(const gh_adapter* p, int32_t* status, void* ws, size_t ws_bytes, void* stream) {
+  g_last_error.clear();
+  gh_status r = check_adapter(p);
+  if (r != GH_OK) return r;
+  if (!status) return fail(GH_ERR_INVALID_ARG, "status is NULL");
+  if (!p->W || !p->A || !p->B || !p->scale) return fail(GH_ERR_INVALID_ARG, "W/A/B/scale is NULL");
+  if (p->N > 0 && (!p->H || !p->adapter_id || !p->logits))
+    return fail(GH_ERR_INVALID_ARG, "H/adapter_id/logits is NULL");
+  const bool bf16 = p->dtype == GH_BF16;
+  if (bf16 && (!aligned16(p->W) || !aligned16(p->A) || !aligned16(p->B) || (p->N > 0 && !aligned16(p->H))))
+    return fail(GH_ERR_INVALID_ARG, "bf16 H, W, A and B must be 16-byte aligned");
+  const size_t elt = p->out_dtype == GH_BF16 ? 2 : 4;
+  if (p->N > 0 && (p->ld < p->V || p->ld > (int64_t(1) << 32)))
+    return fail(GH_ERR_INVALID_ARG, "logits row stride %lld is less than V=%lld or too large", (long long)p->ld,
+                (long long)p->V);
+  if (reinterpret_cast<uintptr_t>(p->logits) % elt != 0)
+    return fail(GH_ERR_INVALID_ARG, "logits is not element-aligned");
+  const size_t need = grpo_adapter_logits_workspace_size(p);
+  if (need > 0 && (!ws || ws_bytes < need))
+    return fail(GH_ERR_WORKSPACE, "adapter workspace needs %zu bytes, got %zu", need, ws ? ws_bytes : size_t(0));
+  if (need > 0 && !aligned16(ws)) return fail(GH_ERR_INVALID_ARG, "ws must be 16-byte aligned");
+  if (!device_is_sm103()) return fail(GH_ERR_UNSUPPORTED, "current device is not an sm_103 (GB300) GPU");
+  if (p->N == 0) return GH_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const AdapterPlan q = adapter_plan(p->N, p->rank, p->num_adapters);
+  AdapterArgs a{};
+  a.N = static_cast<int>(p->N);
+  a.D = static_cast<int>(p->D);
+  a.V = static_cast<int>(p->V);
+  a.rank = p->rank;
+  a.num_adapters = p->num_adapters;
+  a.dtype = p->dtype;
+  a.out_dtype = p->out_dtype;
+  a.H = p->H;
+  a.W = p->W;
+  a.A = p->A;
+  a.B = p->B;
+  a.scale = p->scale;
+  a.ids = p->adapter_id;
+  a.out = p->logits;
+  a.ld = p->ld;
+  a.vec_out = aligned16(p->logits) && p->ld * elt % 16 == 0;
+  a.U = ws;
+  a.list = bf16 ? reinterpret_cast<int32_t*>(static_cast<char*>(ws) + q.u_bytes) : nullptr;
+  a.tile_rows = q.tile_rows;
+  a.rank_chunks = q.rank_chunks;
+  a.max_chunks = q.max_chunks;
+  a.list_ld = q.list_ld;
+  a.status = status;
+  cudaError_t e = run(K_ADAPTER_LOW, st, [&] { return launch_adapter_low(a, st); });
+  if (e != cudaSuccess) return cuda_fail(e, "adapter low-rank launch");
+  e = run(K_ADAPTER_TC, st, [&] { return launch_adapter_logits(a, st); });
+  if (e != cudaSuccess) return cuda_fail(e, "adapter logits launch");
+  return GH_OK;
+}
+
 void gh_profile_enable(int32_t on) {
   std::lock_guard<std::mutex> lk(g_mu);
   g_prof.on = on != 0;
@@ -948,7 +1052,7 @@ const char* gh_kernel_kind_name(int32_t kind) {
       "dw_gemm_tc", "group_advantage", "fwd_logits_lse_f32", "dlogits_f32", "gemm_f32", "timeout_probe",
       "grpo_sequence_totals", "merge_lse_shards", "gspo_partials", "gspo_finish", "dh_merge",
       "dhdw_gemm_tc", "shape_logits", "shaped_logp", "shaped_logp_merge", "shaped_logp_grad", "adapter_low_rank",
-      "adapter_logits_tc"};
+      "adapter_logits"};
   if (kind < 0 || kind >= GH_NUM_KERNEL_KINDS) return "";
   return names[kind];
 }

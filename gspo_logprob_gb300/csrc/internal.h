@@ -61,6 +61,11 @@ inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 bool make_tmap_bf16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
                     uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer);
 
+// bf16 [depth, rows, inner] tensor map read in boxes of 16 elements by box_rows
+// rows, 32-byte swizzle, zero fill out of bounds (strides in bytes).
+bool make_tmap_bf16_k16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint64_t depth,
+                        uint64_t row_stride, uint64_t depth_stride, uint32_t box_rows);
+
 int num_sms();
 uint64_t timeout_ns();
 // Sets the calling thread's gh_last_error() message.
@@ -283,6 +288,36 @@ cudaError_t launch_shape(ShapeArgs a, cudaStream_t st);
 cudaError_t launch_shaped_logp(ShapeArgs a, cudaStream_t st);   // segment partials and target logits
 cudaError_t launch_shaped_merge(ShapeArgs a, cudaStream_t st);  // logp and LSE from them
 cudaError_t launch_shaped_grad(ShapeArgs a, cudaStream_t st);
+
+// --- head with adapters (adapter_kernels.cu) -----------------------------------
+struct AdapterPlan {
+  int tile_rows;    // rows that share a list of adapters (and a tensor-core tile)
+  int rank_chunks;  // 16-wide chunks of a rank
+  int max_chunks;   // chunks a row tile may have
+  int list_ld;
+  int64_t u_rows;   // rows of 16 elements
+  size_t u_bytes, list_bytes;
+};
+AdapterPlan adapter_plan(int64_t N, int64_t rank, int64_t num_adapters);
+struct AdapterArgs {
+  int N, D, V, rank, num_adapters;
+  int dtype, out_dtype;
+  const void* H;
+  const void* W;
+  const void* A;
+  const void* B;
+  const float* scale;
+  const int32_t* ids;
+  void* out;
+  int64_t ld;
+  bool vec_out;  // output rows start on 16-byte boundaries
+  void* U;       // bf16 [u_rows, 16], or fp32 [N, rank]
+  int32_t* list;
+  int tile_rows, rank_chunks, max_chunks, list_ld;
+  int* status;
+};
+cudaError_t launch_adapter_low(const AdapterArgs& a, cudaStream_t st);
+cudaError_t launch_adapter_logits(const AdapterArgs& a, cudaStream_t st);
 
 cudaError_t launch_timeout_probe(int* status, uint64_t timeout_ns, cudaStream_t st);
 

@@ -18,7 +18,7 @@ from typing import Optional
 import torch
 
 from . import _abi
-from ._abi import GhGrpo, GhHead, GhShaping
+from ._abi import GhAdapter, GhGrpo, GhHead, GhShaping
 
 _BF16 = torch.bfloat16
 _F32 = torch.float32
@@ -513,6 +513,67 @@ def grpo_group_advantage(rewards, group_size: int, eps: float = 1e-4, status: Op
                                        _stream(dev))
     _abi.check(code, "grpo_group_advantage")
     return adv
+
+
+# ------------------------------------------------------------------ adapters beside the head
+def padded_logits(rows: int, V: int, dtype: torch.dtype, device) -> torch.Tensor:
+    """[rows, V] logits whose rows start on 16-byte boundaries: the first V
+    columns of a tensor whose width is the next multiple (V itself, and
+    contiguous, where that is one already)."""
+    per = 16 // dtype.itemsize
+    width = (int(V) + per - 1) // per * per
+    t = torch.empty(int(rows), width, dtype=dtype, device=device)
+    return t if width == V else t[:, :V]
+
+
+@_nvtx
+def grpo_adapter_logits(H, W, A, B, scale, adapter_id, *, logits=None, out_dtype=None,
+                        status: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """Logits [N, V] of the head W [V, D] on H [N, D] with row i's adapter a =
+    ``adapter_id[i]`` (int32, -1: none) added: scale[a] B[a] (A[a] h_i), A
+    [adapters, rank, D], B [adapters, V, rank], scale fp32.  bf16 (default
+    output bf16, or ``out_dtype=torch.float32``) or fp32 throughout.
+
+    ``logits`` is a caller's output of any row stride; the default is a
+    ``padded_logits`` tensor.  ``workspace`` as in grpo_head_forward, of
+    grpo_adapter_logits_workspace_size bytes.  Returns a dict with logits, status."""
+    _need(H, "H")
+    _need(W, "W", dtype=H.dtype)
+    dt = _gh_dtype(H.dtype, "H")
+    if H.dim() != 2 or W.dim() != 2 or H.shape[1] != W.shape[1]:
+        raise ValueError("H must be [N, D] and W [V, D]")
+    N, D = H.shape
+    V = W.shape[0]
+    if A.dim() != 3 or B.dim() != 3:
+        raise ValueError("A must be [adapters, rank, D] and B [adapters, V, rank]")
+    n, r = A.shape[0], A.shape[1]
+    _need(A, "A", H.dtype, (n, r, D))
+    _need(B, "B", H.dtype, (n, V, r))
+    _need(scale, "scale", _F32, (n,))
+    _need(adapter_id, "adapter_id", torch.int32, (N,))
+    dev = H.device
+    for name, t in (("W", W), ("A", A), ("B", B), ("scale", scale), ("adapter_id", adapter_id)):
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, H on {dev}")
+    if logits is None:
+        logits = padded_logits(N, V, out_dtype or H.dtype, dev)
+    else:
+        if not logits.is_cuda or logits.device != dev or tuple(logits.shape) != (N, V) or \
+                (V > 1 and logits.stride(1) != 1):
+            raise ValueError(f"logits must be a CUDA tensor on {dev} of shape {(N, V)} with contiguous rows")
+        if out_dtype is not None and logits.dtype != out_dtype:
+            raise TypeError(f"logits must be {out_dtype}, got {logits.dtype}")
+    ld = logits.stride(0) if N > 1 else max(logits.stride(0), V)
+    p = GhAdapter(N, D, V, dt, _gh_dtype(logits.dtype, "logits"), r, n, H.data_ptr(), W.data_ptr(), A.data_ptr(),
+                  B.data_ptr(), scale.data_ptr(), adapter_id.data_ptr(), logits.data_ptr(), ld)
+    ref = ctypes.byref(p)
+    lib = _lib()
+    nbytes = int(lib.grpo_adapter_logits_workspace_size(ref))
+    ws = _caller_workspace(workspace, nbytes) if workspace is not None else WORKSPACE.get(dev, nbytes)
+    st = new_status(dev) if status is None else status
+    code = lib.grpo_adapter_logits(ref, st.data_ptr(), ws.data_ptr(), nbytes, _stream(dev))
+    _abi.check(code, "grpo_adapter_logits")
+    return dict(logits=logits, status=st)
 
 
 # ------------------------------------------------------------------ logit shaping

@@ -375,6 +375,46 @@ gh_status grpo_head_forward_noalloc(const gh_head* head, const gh_grpo* grpo, fl
                                     float* coef, float* loss3, int32_t* status, void* stream);
 
 /*
+ * Logits of a shared head with low-rank adapters, one per row (the requests of
+ * a batch bring their own):
+ *   z_i = W h_i + scale[a] B_a (A_a h_i),   a = adapter_id[i]; -1: W h_i alone.
+ * Rows may come in any order of adapters; rows of a tile (128 rows, or 256 in
+ * calls of more than 128) share one pass over W and over the B_a in use.
+ */
+typedef struct {
+  int64_t N;                 /* rows (tokens), at most 2^24                                 */
+  int64_t D;                 /* hidden size                                                 */
+  int64_t V;                 /* vocabulary size                                             */
+  int32_t dtype;             /* gh_dtype of H, W, A and B: bf16 (tensor cores, fp32
+                                accumulate; D and rank multiples of 8, 16-byte aligned
+                                bases) or fp32 (exact fp32 FMA)                             */
+  int32_t out_dtype;         /* gh_dtype of logits; fp32 when dtype is                      */
+  int32_t rank;              /* low rank of every adapter, at most 256 (pad smaller ones
+                                with zeros)                                                 */
+  int32_t num_adapters;
+  const void* H;             /* [N, D]                                                      */
+  const void* W;             /* [V, D]                                                      */
+  const void* A;             /* [num_adapters, rank, D]                                     */
+  const void* B;             /* [num_adapters, V, rank]                                     */
+  const float* scale;        /* [num_adapters]                                              */
+  const int32_t* adapter_id; /* [N]; outside [-1, num_adapters): GH_DEV_BAD_ROW, taken as -1 */
+  void* logits;              /* [N, V] out, any row stride ld >= V in elements; rows on
+                                16-byte boundaries are the fast case                        */
+  int64_t ld;
+} gh_adapter;
+
+/* Bytes of scratch `ws` grpo_adapter_logits needs (0 for invalid arguments). */
+size_t grpo_adapter_logits_workspace_size(const gh_adapter* problem);
+/*
+ * A bf16 call sums each A_a h_i in fp32 and carries it as two bf16 terms, so
+ * that the logits have the accuracy of fp32 accumulation whatever out_dtype.
+ * A row's logits do not depend on the other rows' values or adapters as long
+ * as the weights are finite: the rows of a tile multiply the B_a of the
+ * others by zero, so a NaN or infinity in a B_a in use reaches all of them.
+ */
+gh_status grpo_adapter_logits(const gh_adapter* problem, int32_t* status, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * How the logits of a batch are shaped before they are a distribution, as
  * samplers do: penalties for repeated tokens, biases, allow (grammar) masks and
  * a temperature, each per row.  With h the row's history (its first prompt_len
