@@ -30,6 +30,17 @@ namespace {
 constexpr int AD_THREADS = 256;
 constexpr int AD_RANKS = 8;  // ranks per CTA: one per warp
 
+// acc + the dot product of eight bf16 pairs
+__device__ __forceinline__ float ad_dot8(const uint4& x, const uint4& y, float acc) {
+  const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    acc = fmaf(__uint_as_float(xw[i] << 16), __uint_as_float(yw[i] << 16), acc);
+    acc = fmaf(__uint_as_float(xw[i] & 0xffff0000u), __uint_as_float(yw[i] & 0xffff0000u), acc);
+  }
+  return acc;
+}
+
 // One CTA: RPC consecutive rows (of one row tile) times 8 ranks.  It finds the
 // adapters of the row tile in the order of their first rows (the tile's slots),
 // and writes its rows' part of every slot's chunk: u in their own slot, 0 in the
@@ -48,6 +59,7 @@ __global__ void __launch_bounds__(AD_THREADS) adapter_low_kernel(const AdapterAr
   const int row0 = blockIdx.x * RPC;
   const int tile = row0 / a.tile_rows, base = tile * a.tile_rows;
   const int j = blockIdx.y * AD_RANKS + warp;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product may start beside this launch
 
   int id = -1;
   if (tid < a.tile_rows && base + tid < a.N) {
@@ -75,28 +87,33 @@ __global__ void __launch_bounds__(AD_THREADS) adapter_low_kernel(const AdapterAr
       const size_t astep = static_cast<size_t>(a.rank) * a.D;
       const __nv_bfloat16* A0 = static_cast<const __nv_bfloat16*>(a.A) + static_cast<size_t>(j) * a.D;
       const __nv_bfloat16* H0 = static_cast<const __nv_bfloat16*>(a.H) + static_cast<size_t>(row0) * a.D;
-#pragma unroll 4
-      for (int k = lane * 8; k < a.D; k += 256) {
-        float w[8];
+      bool one = true;  // the rows have one adapter: its row of A is read once for all of them
 #pragma unroll
+      for (int q = 1; q < RPC; ++q) one &= rid[q] == rid[0];
+      if (one) {
+        const __nv_bfloat16* A1 = A0 + rid[0] * astep;
+#pragma unroll 2
+        for (int k = lane * 8; k < a.D; k += 256) {
+          const uint4 w = __ldg(reinterpret_cast<const uint4*>(A1 + k));
+          uint4 h[RPC];
+#pragma unroll
+          for (int q = 0; q < RPC; ++q) h[q] = __ldg(reinterpret_cast<const uint4*>(H0 + static_cast<size_t>(q) * a.D + k));
+#pragma unroll
+          for (int q = 0; q < RPC; ++q) acc[q] = ad_dot8(w, h[q], acc[q]);
+        }
+      } else {
+#pragma unroll 1
         for (int q = 0; q < RPC; ++q) {
-          if (rid[q] < 0) continue;
-          if (q == 0 || rid[q] != rid[q - 1]) {
-            const uint4 t = __ldg(reinterpret_cast<const uint4*>(A0 + rid[q] * astep + k));
-            const uint32_t tw[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              w[2 * i] = __uint_as_float(tw[i] << 16);
-              w[2 * i + 1] = __uint_as_float(tw[i] & 0xffff0000u);
-            }
+          float s = 0.f;
+          const int i = ids[row0 - base + q];
+          if (i >= 0) {
+#pragma unroll 4
+            for (int k = lane * 8; k < a.D; k += 256)
+              s = ad_dot8(__ldg(reinterpret_cast<const uint4*>(A0 + i * astep + k)),
+                          __ldg(reinterpret_cast<const uint4*>(H0 + static_cast<size_t>(q) * a.D + k)), s);
           }
-          const uint4 t = __ldg(reinterpret_cast<const uint4*>(H0 + static_cast<size_t>(q) * a.D + k));
-          const uint32_t hw[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            acc[q] = fmaf(w[2 * i], __uint_as_float(hw[i] << 16), acc[q]);
-            acc[q] = fmaf(w[2 * i + 1], __uint_as_float(hw[i] & 0xffff0000u), acc[q]);
-          }
+          for (int t = 0; t < RPC; ++t) acc[t] = t == q ? s : acc[t];
         }
       }
 #pragma unroll
@@ -190,25 +207,36 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
-// PAIR = false: a CTA computes 128 rows by bn columns (up to 256): decode, where
-// every CTA streams its own W tiles.  PAIR = true: two CTAs share a 256 x 256 tile
+// PAIR = false: a CTA computes 128 rows by bn columns: decode, where every CTA
+// streams its own W tiles.  PAIR = true: two CTAs share a 256-row tile
 // (cta_group::2), each staging its 128 rows of H and its half of the W tile:
 // prompts, where the operands' L2 traffic per FLOP counts.
-template <bool PAIR>
+//
+// EXACT (fp32 logits): the tensor cores truncate when they add to the
+// accumulator, about half an ulp per K = 16 step towards zero (1.3e-6 of the
+// logits at D = 1000, growing with D), so K is cut into segments of SEG_KB
+// blocks, each its own accumulator, which the epilogue adds up in registers with
+// rounding to nearest (3e-7).  A thread then holds a row of the tile: 128 columns
+// per tile, not 256.  bf16 logits round by 2^-9 anyway and keep one accumulator.
+template <bool PAIR, bool EXACT>
 struct AdCfg {
+  static constexpr int BN = EXACT ? 128 : TC_BN;  // widest tile
+  static constexpr int NUM_ACC = TC_TMEM_COLS / BN;
+  static constexpr int SEG_KB = 8;  // EXACT: 64-wide K blocks per accumulator
   static constexpr int A_BYTES = TC_BM * TC_BK * 2;
-  static constexpr int B_ROWS = PAIR ? TC_BN / 2 : TC_BN;
+  static constexpr int B_ROWS = PAIR ? BN / 2 : BN;
   static constexpr int STAGE_BYTES = A_BYTES + B_ROWS * TC_BK * 2;
-  static constexpr int STAGES = PAIR ? 6 : 4;  // 192 KB in flight per SM
-  static constexpr int U_BYTES = TC_BM * 32;   // one term of a chunk
+  static constexpr int STAGES = 192 * 1024 / STAGE_BYTES;  // 192 KB in flight per SM
+  static constexpr int U_BYTES = TC_BM * 32;  // one term of a chunk
   static constexpr int CHUNK_BYTES = 2 * U_BYTES + B_ROWS * 32;
   static constexpr int CHUNKS = 2;  // low-rank chunks per stage
   static constexpr int EPI_WARPS = 4;
   static constexpr int THREADS = 64 + 32 * EPI_WARPS;
   static constexpr int TURN_LD = 33;  // fp32 transpose tile of an epilogue warp
   static constexpr int TURN_BYTES = 32 * TURN_LD * 4;
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_WARPS * TURN_BYTES + 1024 + 256;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_WARPS * TURN_BYTES + 1024 + 512;
   static_assert(CHUNKS * CHUNK_BYTES <= STAGE_BYTES, "chunks share the stages");
+  static_assert((2 * STAGES + 2 * NUM_ACC + 1) * 8 + 8 <= 512, "barriers");
 };
 
 // 32 columns of a row per thread to the output; rows of a warp are consecutive.
@@ -257,20 +285,20 @@ __device__ __forceinline__ void ad_store(const AdapterArgs& a, const float* v, i
   }
 }
 
-template <bool PAIR, class TOut>
-__global__ void __launch_bounds__(AdCfg<PAIR>::THREADS, 1)
+template <bool PAIR, bool EXACT, class TOut>
+__global__ void __launch_bounds__(AdCfg<PAIR, EXACT>::THREADS, 1)
     adapter_tc_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CUtensorMap tmW,
                       const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmB, const TcSched sc,
                       const int bn, const AdapterArgs a, const uint64_t timeout_ns) {
-  using C = AdCfg<PAIR>;
+  using C = AdCfg<PAIR, EXACT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* turn_all = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE_BYTES);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::STAGE_BYTES + C::EPI_WARPS * C::TURN_BYTES);
   uint64_t* empty = full + C::STAGES;
   uint64_t* tfull = empty + C::STAGES;
-  uint64_t* tempty = tfull + 2;
-  uint64_t* drain = tempty + 2;
+  uint64_t* tempty = tfull + C::NUM_ACC;
+  uint64_t* drain = tempty + C::NUM_ACC;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -282,7 +310,7 @@ __global__ void __launch_bounds__(AdCfg<PAIR>::THREADS, 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < C::NUM_ACC; ++b) {
       mbar_init(&tfull[b], 1);
       mbar_init(&tempty[b], (PAIR ? 2 : 1) * C::EPI_WARPS);
     }
@@ -319,7 +347,7 @@ __global__ void __launch_bounds__(AdCfg<PAIR>::THREADS, 1)
       int stage = 0;
       uint32_t phase = 0;
       uint32_t pending = 0, pend_par = 0;  // per stage: load issued and its phase parity
-      bool ok = true, issued = false;
+      bool ok = true, issued = false, waited = false;
       const auto open_stage = [&](uint32_t bytes) {
         if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, a.status, GH_DEV_TIMEOUT, timeout_ns)) {
           ok = false;
@@ -357,7 +385,7 @@ __global__ void __launch_bounds__(AdCfg<PAIR>::THREADS, 1)
         int m_blk, n_blk;
         tc_task_of(sc, task, m_blk, n_blk);
         const int m0 = m_blk * sc.m_step + static_cast<int>(rank) * TC_BM;
-        const int n0 = n_blk * bn + static_cast<int>(rank) * (TC_BN / 2);
+        const int n0 = n_blk * bn + static_cast<int>(rank) * C::B_ROWS;
         const int b_rows = PAIR ? C::B_ROWS : bn;
         for (int kb = 0; kb < sc.num_kb; ++kb) {
           if (!open_stage(C::A_BYTES + b_rows * TC_BK * 2)) break;
@@ -365,6 +393,11 @@ __global__ void __launch_bounds__(AdCfg<PAIR>::THREADS, 1)
           load2(s, &tmH, kb * TC_BK, m0);
           load2(s + C::A_BYTES, &tmW, kb * TC_BK, n0);
           close_stage();
+        }
+        if (!waited) {
+          // u and the lists are the launch's before; u is read by the asynchronous proxy
+          asm volatile("griddepcontrol.wait;\n\tfence.proxy.async;" ::: "memory");
+          waited = true;
         }
         const int* list = a.list + static_cast<size_t>(m_blk) * a.list_ld;
         const int chunks = ok ? list[0] * rc : 0;
@@ -382,6 +415,8 @@ __global__ void __launch_bounds__(AdCfg<PAIR>::THREADS, 1)
           close_stage();
         }
       }
+      // this launch is not over before the one that it depends on
+      if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
       if (!ok) {
         if (PAIR) {
           // completions land on the even CTA's barriers, which this CTA cannot
@@ -401,12 +436,12 @@ __global__ void __launch_bounds__(AdCfg<PAIR>::THREADS, 1)
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       // ------------------------------------------------ MMA issuer
-      const uint32_t idesc = PAIR ? idesc_bf16_f32(2 * TC_BM, TC_BN, false, false) : idesc_bf16_f32(TC_BM, bn, false, false);
+      const uint32_t idesc = PAIR ? idesc_bf16_f32(2 * TC_BM, C::BN, false, false) : idesc_bf16_f32(TC_BM, bn, false, false);
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
       uint32_t acc_phase = 0;
-      bool ok = true, issued = false;
+      bool ok = true, issued = false, waited = false;
       const auto wait_stage = [&] {
         if (!mbar_wait_bounded(&full[stage], phase, abort_flag, a.status, GH_DEV_TIMEOUT, timeout_ns)) {
           ok = false;
@@ -435,19 +470,43 @@ __global__ void __launch_bounds__(AdCfg<PAIR>::THREADS, 1)
       for (int task = cid; ok && task < sc.num_tasks; task += ncl) {
         int m_blk, n_blk;
         tc_task_of(sc, task, m_blk, n_blk);
-        if (!mbar_wait_bounded(&tempty[acc], acc_phase ^ 1u, abort_flag, a.status, GH_DEV_TIMEOUT, timeout_ns)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d = tmem_base + static_cast<uint32_t>(acc * TC_BN);
+        uint32_t d = 0;
+        const auto open_acc = [&] {
+          if (!mbar_wait_bounded(&tempty[acc], acc_phase ^ 1u, abort_flag, a.status, GH_DEV_TIMEOUT, timeout_ns)) {
+            ok = false;
+            return false;
+          }
+          tc_fence_after();
+          d = tmem_base + static_cast<uint32_t>(acc * C::BN);
+          return true;
+        };
+        const auto close_acc = [&] {
+          if (PAIR)
+            umma_pair_commit_mc(&tfull[acc], 0x3);
+          else
+            umma_commit(&tfull[acc]);
+          if (++acc == C::NUM_ACC) {
+            acc = 0;
+            acc_phase ^= 1u;
+          }
+        };
         for (int kb = 0; kb < sc.num_kb; ++kb) {
+          const bool first = EXACT ? kb % C::SEG_KB == 0 : kb == 0;
+          if (first) {
+            if (kb > 0) close_acc();
+            if (!open_acc()) break;
+          }
           if (!wait_stage()) break;
           const uint32_t ab = smem_u32(smem + stage * C::STAGE_BYTES), bb = ab + C::A_BYTES;
 #pragma unroll
           for (int kk = 0; kk < TC_BK / 16; ++kk)
-            mma(d, sdesc_sw128(ab + kk * 32, 16, 1024), sdesc_sw128(bb + kk * 32, 16, 1024), (kb | kk) != 0 ? 1u : 0u);
+            mma(d, sdesc_sw128(ab + kk * 32, 16, 1024), sdesc_sw128(bb + kk * 32, 16, 1024), !first || kk != 0 ? 1u : 0u);
           free_stage();
+        }
+        // the adapters, in the last accumulator
+        if (!waited) {
+          asm volatile("griddepcontrol.wait;" ::: "memory");
+          waited = true;
         }
         const int chunks = ok ? a.list[static_cast<size_t>(m_blk) * a.list_ld] * rc : 0;
         for (int c0 = 0; ok && c0 < chunks; c0 += C::CHUNKS) {
@@ -462,12 +521,7 @@ __global__ void __launch_bounds__(AdCfg<PAIR>::THREADS, 1)
           free_stage();
         }
         if (!ok) break;
-        if (PAIR)
-          umma_pair_commit_mc(&tfull[acc], 0x3);
-        else
-          umma_commit(&tfull[acc]);
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1u;
+        close_acc();
       }
       if (issued) {
         // every MMA issued must be complete before TMEM is freed
@@ -486,22 +540,7 @@ __global__ void __launch_bounds__(AdCfg<PAIR>::THREADS, 1)
     float* turn = turn_all + (warp - 2) * (C::TURN_BYTES / 4);
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int task = cid; task < sc.num_tasks; task += ncl) {
-      int m_blk, n_blk;
-      tc_task_of(sc, task, m_blk, n_blk);
-      if (!warp_wait(&tfull[acc], acc_phase, abort_flag, a.status, timeout_ns)) break;
-      tc_fence_after();
-      const int row = m_blk * sc.m_step + static_cast<int>(rank) * TC_BM + sub * 32 + lane;
-      if (row - lane < a.N) {
-#pragma unroll 1
-        for (int c = 0; c < bn / 32; ++c) {
-          const int col0 = n_blk * bn + c * 32;
-          if (col0 >= a.V) break;
-          float v[32];
-          tmem_ld32(tmem_base + lane_addr + static_cast<uint32_t>(acc * TC_BN + c * 32), v);
-          ad_store<TOut>(a, v, row, col0, lane, turn);
-        }
-      }
+    const auto free_acc = [&] {
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -510,8 +549,60 @@ __global__ void __launch_bounds__(AdCfg<PAIR>::THREADS, 1)
         else
           mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
       }
-      acc ^= 1;
-      if (acc == 0) acc_phase ^= 1u;
+      if (++acc == C::NUM_ACC) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    };
+    bool ok = true;
+    for (int task = cid; ok && task < sc.num_tasks; task += ncl) {
+      int m_blk, n_blk;
+      tc_task_of(sc, task, m_blk, n_blk);
+      const int row = m_blk * sc.m_step + static_cast<int>(rank) * TC_BM + sub * 32 + lane;
+      const bool rows = row - lane < a.N;  // the warp has rows
+      if constexpr (EXACT) {
+        float z[C::BN];
+        for (int kb = 0; ok && kb < sc.num_kb; kb += C::SEG_KB) {
+          if (!warp_wait(&tfull[acc], acc_phase, abort_flag, a.status, timeout_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (rows) {
+#pragma unroll
+            for (int c = 0; c < C::BN / 32; ++c) {
+              if (c * 32 < bn) {
+                float v[32];
+                tmem_ld32(tmem_base + lane_addr + static_cast<uint32_t>(acc * C::BN + c * 32), v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) z[c * 32 + i] = kb == 0 ? v[i] : z[c * 32 + i] + v[i];
+              }
+            }
+          }
+          free_acc();
+        }
+        if (ok && rows) {
+#pragma unroll
+          for (int c = 0; c < C::BN / 32; ++c) {
+            const int col0 = n_blk * bn + c * 32;
+            if (c * 32 < bn && col0 < a.V) ad_store<TOut>(a, z + c * 32, row, col0, lane, turn);
+          }
+        }
+      } else {
+        if (!warp_wait(&tfull[acc], acc_phase, abort_flag, a.status, timeout_ns)) break;
+        tc_fence_after();
+        if (rows) {
+#pragma unroll 1
+          for (int c = 0; c < bn / 32; ++c) {
+            const int col0 = n_blk * bn + c * 32;
+            if (col0 >= a.V) break;
+            float v[32];
+            tmem_ld32(tmem_base + lane_addr + static_cast<uint32_t>(acc * C::BN + c * 32), v);
+            ad_store<TOut>(a, v, row, col0, lane, turn);
+          }
+        }
+        free_acc();
+      }
     }
   }
 
@@ -610,10 +701,10 @@ __global__ void __launch_bounds__(256) adapter_f32_kernel(const AdapterArgs a) {
 
 // columns per tile of the single-CTA form: the widest of those that cost the
 // fewest columns in the longest CTA (a tile re-reads the rows of H, half as dear)
-int decode_cols(int N, int V) {
-  int best = 256;
+int decode_cols(int N, int V, int widest) {
+  int best = widest;
   int64_t cost = -1;
-  for (int bn = 256; bn >= 32; bn -= 32) {
+  for (int bn = widest; bn >= 32; bn -= 32) {
     const int64_t c = ceil_div(ceil_div(V, bn), num_sms()) * (2 * bn + (N < TC_BM ? N : TC_BM));
     if (cost < 0 || c < cost) {
       cost = c;
@@ -623,49 +714,59 @@ int decode_cols(int N, int V) {
   return best;
 }
 
+// Set-up of a kernel, done once per device under a lock.
 struct AdSetup {
   std::mutex mu;
   bool done[64] = {};
   int pairs[64] = {};
 };
+int this_device() {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  return dev < 0 || dev >= 64 ? 0 : dev;
+}
+template <class F>
+cudaError_t once_per_device(AdSetup& s, F&& f) {
+  const int dev = this_device();
+  std::lock_guard<std::mutex> g(s.mu);
+  if (s.done[dev]) return cudaSuccess;
+  const cudaError_t e = f();
+  s.done[dev] = e == cudaSuccess;
+  return e;
+}
 
 template <bool PAIR, class TOut>
 cudaError_t launch_product(const AdapterArgs& a, cudaStream_t st) {
-  using C = AdCfg<PAIR>;
-  auto kern = adapter_tc_kernel<PAIR, TOut>;
+  constexpr bool EXACT = sizeof(TOut) == 4;
+  using C = AdCfg<PAIR, EXACT>;
+  auto kern = adapter_tc_kernel<PAIR, EXACT, TOut>;
   static AdSetup setup;
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64) dev = 0;
-  int pairs_fit;
-  {
-    std::lock_guard<std::mutex> g(setup.mu);
-    if (!setup.done[dev]) {
-      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
-      if (e != cudaSuccess) return e;
-      int n = num_sms() / 2;
-      if (PAIR) {
-        cudaLaunchConfig_t q = {};
-        q.gridDim = dim3(2 * n);
-        q.blockDim = dim3(C::THREADS);
-        q.dynamicSmemBytes = C::SMEM_BYTES;
-        cudaLaunchAttribute qa[1];
-        qa[0].id = cudaLaunchAttributeClusterDimension;
-        qa[0].val.clusterDim.x = 2;
-        qa[0].val.clusterDim.y = 1;
-        qa[0].val.clusterDim.z = 1;
-        q.attrs = qa;
-        q.numAttrs = 1;
-        int fit = 0;
-        if (cudaOccupancyMaxActiveClusters(&fit, kern, &q) == cudaSuccess && fit > 0 && fit < n) n = fit;
-        (void)cudaGetLastError();
-      }
-      setup.pairs[dev] = n > 0 ? n : 1;
-      setup.done[dev] = true;
+  cudaError_t e = once_per_device(setup, [&] {
+    cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    if (r != cudaSuccess) return r;
+    int n = num_sms() / 2;
+    if (PAIR) {  // the pairs that fit on the device
+      cudaLaunchConfig_t q = {};
+      q.gridDim = dim3(2 * n);
+      q.blockDim = dim3(C::THREADS);
+      q.dynamicSmemBytes = C::SMEM_BYTES;
+      cudaLaunchAttribute qa[1];
+      qa[0].id = cudaLaunchAttributeClusterDimension;
+      qa[0].val.clusterDim.x = 2;
+      qa[0].val.clusterDim.y = 1;
+      qa[0].val.clusterDim.z = 1;
+      q.attrs = qa;
+      q.numAttrs = 1;
+      int fit = 0;
+      if (cudaOccupancyMaxActiveClusters(&fit, kern, &q) == cudaSuccess && fit > 0 && fit < n) n = fit;
+      (void)cudaGetLastError();
     }
-    pairs_fit = setup.pairs[dev];
-  }
-  const int bn = PAIR ? TC_BN : decode_cols(a.N, a.V);
+    setup.pairs[this_device()] = n > 0 ? n : 1;
+    return cudaSuccess;
+  });
+  if (e != cudaSuccess) return e;
+  const int pairs_fit = setup.pairs[this_device()];
+  const int bn = PAIR ? C::BN : decode_cols(a.N, a.V, C::BN);
   const uint32_t b_rows = PAIR ? C::B_ROWS : bn;
   CUtensorMap th, tw, tu, tb;
   const uint64_t row_bytes = static_cast<uint64_t>(a.D) * 2;
@@ -693,14 +794,17 @@ cudaError_t launch_product(const AdapterArgs& a, cudaStream_t st) {
   cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM_BYTES;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  // the product starts while u is computed and waits for it at its first chunk
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = PAIR ? 1 : 0;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, th, tw, tu, tb, sc, bn, a, timeout_ns());
+  cfg.numAttrs = PAIR ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, kern, th, tw, tu, tb, sc, bn, a, timeout_ns());
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
@@ -727,6 +831,17 @@ cudaError_t launch_adapter_low(const AdapterArgs& a, cudaStream_t st) {
     const int64_t warps = static_cast<int64_t>(a.N) * a.rank;
     adapter_low_f32_kernel<<<static_cast<unsigned>(ceil_div(warps, 8)), 256, 0, st>>>(a);
   } else {
+    // Both forms ask for the shared memory split of the product: an SM has to be idle to change its split, and the
+    // product could not start beside this launch.
+    static AdSetup setup;
+    cudaError_t e = once_per_device(setup, [] {
+      cudaError_t r = cudaFuncSetAttribute(adapter_low_kernel<1>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                           cudaSharedmemCarveoutMaxShared);
+      return r != cudaSuccess ? r
+                              : cudaFuncSetAttribute(adapter_low_kernel<8>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                                     cudaSharedmemCarveoutMaxShared);
+    });
+    if (e != cudaSuccess) return e;
     const unsigned y = static_cast<unsigned>(2 * a.rank_chunks);
     if (a.N < 1024)
       adapter_low_kernel<1><<<dim3(a.N, y), AD_THREADS, 0, st>>>(a);

@@ -38,6 +38,8 @@
 // rows per CTA, the strides or the other rows of the batch.
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -946,9 +948,16 @@ cudaError_t launch_typed(const ShapeArgs& a, cudaStream_t st) {
     return cols / 32 * 10 + SH_SET * 4 + SH_WARPS * (SH_STAGES + (OUT_TILE ? 1 : 0)) * SH_TILE;
   };
   const auto kernel = shape_kernel<TIn, TOut, MODE, ALIGNED, OUT_TILE, MASKS>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes(SH_MAX_COLS)));
+  static std::atomic<uint64_t> ready{0};  // a bit per device whose limit is set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (!(ready.load() & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes(SH_MAX_COLS)));
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit);
+  }
   const int64_t blocks = static_cast<int64_t>(a.ntiles) * ceil_div(a.R, a.rows_per_cta);
   kernel<<<static_cast<unsigned>(blocks), SH_THREADS, bytes(a.cols), st>>>(a);
   return cudaGetLastError();

@@ -571,7 +571,7 @@ def grpo_adapter_logits(H, W, A, B, scale, adapter_id, *, logits=None, out_dtype
     nbytes = int(lib.grpo_adapter_logits_workspace_size(ref))
     ws = _caller_workspace(workspace, nbytes) if workspace is not None else WORKSPACE.get(dev, nbytes)
     st = new_status(dev) if status is None else status
-    code = lib.grpo_adapter_logits(ref, st.data_ptr(), ws.data_ptr(), nbytes, _stream(dev))
+    code = lib.grpo_adapter_logits(ref, st.data_ptr(), ws.data_ptr(), nbytes, _raw_stream(dev))
     _abi.check(code, "grpo_adapter_logits")
     return dict(logits=logits, status=st)
 
@@ -659,6 +659,17 @@ def make_shaping(rows: int, V: int, *, tokens=None, hist_begin=None, hist_len=No
     return Shaping(s, t, dev)
 
 
+_RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(dev: torch.device) -> int:
+    """The current stream's handle as an integer: without a Stream object where
+    torch has a call for that (about 1 us less per call)."""
+    if _RAW_STREAM is not None and dev.index is not None:
+        return _RAW_STREAM(dev.index)
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
 def _gh_dtype(t: torch.dtype, name: str) -> int:
     if t == _BF16:
         return _abi.GH_BF16
@@ -700,7 +711,7 @@ def grpo_shape_logits(logits, shaping: Shaping, *, out=None, out_dtype=None, sta
     dev = logits.device
     st = new_status(dev) if status is None else status
     code = _lib().grpo_shape_logits(shaping.ref, logits.data_ptr(), dt, ld, out.data_ptr(), odt, old, st.data_ptr(),
-                                    _stream(dev))
+                                    _raw_stream(dev))
     _abi.check(code, "grpo_shape_logits")
     return dict(logits=out, status=st)
 
@@ -727,7 +738,7 @@ def grpo_shaped_logp(logits, targets, mask, shaping: Shaping, *, out: Optional[d
     ws = _caller_workspace(workspace, nbytes) if workspace is not None else WORKSPACE.get(dev, nbytes)
     code = _lib().grpo_shaped_logp(shaping.ref, logits.data_ptr(), dt, ld, targets.data_ptr(), mask.data_ptr(),
                                    logp.data_ptr(), lse.data_ptr(), st.data_ptr(), ws.data_ptr(), nbytes,
-                                   _stream(dev))
+                                   _raw_stream(dev))
     _abi.check(code, "grpo_shaped_logp")
     out.update(logp=logp, lse=lse, status=st)
     return out
@@ -756,7 +767,7 @@ def grpo_shaped_logp_backward(logits, targets, mask, shaping: Shaping, lse, coef
     code = _lib().grpo_shaped_logp_backward(shaping.ref, logits.data_ptr(), dt, ld, targets.data_ptr(),
                                             mask.data_ptr(), lse.data_ptr(), coef.data_ptr(),
                                             None if grad_out is None else grad_out.data_ptr(), dlogits.data_ptr(), dld,
-                                            st.data_ptr(), _stream(dev))
+                                            st.data_ptr(), _raw_stream(dev))
     _abi.check(code, "grpo_shaped_logp_backward")
     return dict(dlogits=dlogits, status=st)
 
