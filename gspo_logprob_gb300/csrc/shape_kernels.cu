@@ -349,14 +349,16 @@ __device__ int sh_build(const ShapeArgs& a, const ShSet& set, const ShRow& first
 #pragma unroll
   for (int i = 0; i < SH_KEEP; ++i) {
     const int k = tid + i * SH_THREADS;
-    kept[i] = k < last.len ? static_cast<uint32_t>(h[k] - c0) : ~0u;
+    kept[i] = ~0u;
+    if (k < last.len) kept[i] = static_cast<uint32_t>(h[k] - c0);
   }
   const auto mark = [&](uint32_t j) {
     if (j < static_cast<uint32_t>(cols)) atomicOr(&set.member[j >> 5], 1u << (j & 31));
   };
   mark(bias_j);
 #pragma unroll
-  for (int i = 0; i < SH_KEEP; ++i) mark(kept[i]);
+  for (int i = 0; i < SH_KEEP; ++i)
+    if (i * SH_THREADS < last.len) mark(kept[i]);
 #pragma unroll 4
   for (int k = tid + SH_KEEP * SH_THREADS; k < last.len; k += SH_THREADS) mark(static_cast<uint32_t>(h[k] - c0));
   for (int k = bk + SH_THREADS; k < last.bias_e; k += SH_THREADS) mark(static_cast<uint32_t>(a.s.bias_tokens[k] - c0));
@@ -401,6 +403,7 @@ __device__ int sh_build(const ShapeArgs& a, const ShSet& set, const ShRow& first
   }
 #pragma unroll
   for (int i = 0; i < SH_KEEP; ++i) {
+    if (i * SH_THREADS >= first.len) break;
     const int k = tid + i * SH_THREADS;
     if (k < first.len && kept[i] < static_cast<uint32_t>(cols)) sh_count(set, kept[i], k < first.plen);
   }

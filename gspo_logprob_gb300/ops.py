@@ -81,6 +81,24 @@ def _need(t: torch.Tensor, name: str, dtype=None, shape=None):
     return t
 
 
+_RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(dev: torch.device) -> int:
+    """The current stream's handle as an integer: without a Stream object where
+    torch has a call for that (about 1 us less per call)."""
+    if _RAW_STREAM is not None and dev.index is not None:
+        return _RAW_STREAM(dev.index)
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _is(t, name: str, dtype, shape):
+    """_need for the calls of a decode step: one expression when all is well."""
+    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t
+    return _need(t, name, dtype, shape)
+
+
 class _Workspace:
     """Grow-only scratch buffer per device, reused by consecutive calls.
 
@@ -95,16 +113,16 @@ class _Workspace:
 
     def get(self, dev: torch.device, nbytes: int) -> torch.Tensor:
         key = (dev.type, dev.index)
-        cur = torch.cuda.current_stream(dev)
+        cur = _raw_stream(dev)
         entry = self._buf.get(key)
-        if entry is None or entry[0].numel() < nbytes:
+        if entry is None or entry[2] < nbytes:
             b = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
-            entry = (b, {cur.cuda_stream})
+            entry = (b, {cur}, b.numel())
             self._buf[key] = entry
-        b, seen = entry
-        if cur.cuda_stream not in seen:
-            b.record_stream(cur)
-            seen.add(cur.cuda_stream)
+        b, seen, _ = entry
+        if cur not in seen:
+            b.record_stream(torch.cuda.current_stream(dev))
+            seen.add(cur)
         return b
 
     def clear(self):
@@ -538,7 +556,6 @@ def grpo_adapter_logits(H, W, A, B, scale, adapter_id, *, logits=None, out_dtype
     ``padded_logits`` tensor.  ``workspace`` as in grpo_head_forward, of
     grpo_adapter_logits_workspace_size bytes.  Returns a dict with logits, status."""
     _need(H, "H")
-    _need(W, "W", dtype=H.dtype)
     dt = _gh_dtype(H.dtype, "H")
     if H.dim() != 2 or W.dim() != 2 or H.shape[1] != W.shape[1]:
         raise ValueError("H must be [N, D] and W [V, D]")
@@ -546,15 +563,15 @@ def grpo_adapter_logits(H, W, A, B, scale, adapter_id, *, logits=None, out_dtype
     V = W.shape[0]
     if A.dim() != 3 or B.dim() != 3:
         raise ValueError("A must be [adapters, rank, D] and B [adapters, V, rank]")
-    n, r = A.shape[0], A.shape[1]
-    _need(A, "A", H.dtype, (n, r, D))
-    _need(B, "B", H.dtype, (n, V, r))
-    _need(scale, "scale", _F32, (n,))
-    _need(adapter_id, "adapter_id", torch.int32, (N,))
+    n, r, _ = A.shape
+    _is(W, "W", H.dtype, (V, D))
+    _is(A, "A", H.dtype, (n, r, D))
+    _is(B, "B", H.dtype, (n, V, r))
+    _is(scale, "scale", _F32, (n,))
+    _is(adapter_id, "adapter_id", torch.int32, (N,))
     dev = H.device
-    for name, t in (("W", W), ("A", A), ("B", B), ("scale", scale), ("adapter_id", adapter_id)):
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, H on {dev}")
+    if not W.device == A.device == B.device == scale.device == adapter_id.device == dev:
+        raise ValueError(f"W, A, B, scale and adapter_id must be on H's device ({dev})")
     if logits is None:
         logits = padded_logits(N, V, out_dtype or H.dtype, dev)
     else:
@@ -586,6 +603,8 @@ class Shaping:
         self.tensors = tensors
         self.device = device
         self.ref = ctypes.byref(struct)
+        self.rows = torch.Size((struct.rows,))
+        self.shape = torch.Size((struct.rows, struct.V))
         self.workspace_bytes = int(_lib().grpo_shaped_logp_workspace_size(self.ref))
 
 
@@ -659,17 +678,6 @@ def make_shaping(rows: int, V: int, *, tokens=None, hist_begin=None, hist_len=No
     return Shaping(s, t, dev)
 
 
-_RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _raw_stream(dev: torch.device) -> int:
-    """The current stream's handle as an integer: without a Stream object where
-    torch has a call for that (about 1 us less per call)."""
-    if _RAW_STREAM is not None and dev.index is not None:
-        return _RAW_STREAM(dev.index)
-    return torch.cuda.current_stream(dev).cuda_stream
-
-
 def _gh_dtype(t: torch.dtype, name: str) -> int:
     if t == _BF16:
         return _abi.GH_BF16
@@ -686,15 +694,17 @@ def _need_logits(t: torch.Tensor, name: str, shaping: Shaping, dtype=None):
         raise ValueError(f"{name} must be a CUDA tensor")
     if shaping.device is not None and t.device != shaping.device:
         raise ValueError(f"{name} is on {t.device}, the shaping on {shaping.device}")
-    s = shaping.struct
-    if tuple(t.shape) != (s.rows, s.V):
-        raise ValueError(f"{name} must have shape {(s.rows, s.V)}, got {tuple(t.shape)}")
-    if s.V > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must have contiguous rows")
+    if t.shape != shaping.shape:
+        raise ValueError(f"{name} must have shape {tuple(shaping.shape)}, got {tuple(t.shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    ld = t.stride(0) if s.rows > 1 else max(s.V, 1)
-    if ld < s.V:
+    rows, V = shaping.shape
+    ld, step = t.stride()
+    if V > 1 and step != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if rows <= 1:
+        ld = max(V, 1)
+    elif ld < V:
         raise ValueError(f"{name} has rows that overlap")
     return _gh_dtype(t.dtype, name), ld
 
@@ -724,15 +734,14 @@ def grpo_shaped_logp(logits, targets, mask, shaping: Shaping, *, out: Optional[d
     hold preallocated logp and lse; ``workspace`` as in grpo_head_forward
     (``shaping.workspace_bytes`` bytes).  Returns a dict with logp, lse, status."""
     dt, ld = _need_logits(logits, "logits", shaping)
-    R = shaping.struct.rows
-    _need(targets, "targets", torch.int32, (R,))
-    _need(mask, "mask", torch.uint8, (R,))
+    R = shaping.rows
+    _is(targets, "targets", torch.int32, R)
+    _is(mask, "mask", torch.uint8, R)
     dev = logits.device
     out = {} if out is None else out
-    logp = _need(out["logp"], "logp", _F32, (R,)) if out.get("logp") is not None else \
-        torch.empty(R, dtype=_F32, device=dev)
-    lse = _need(out["lse"], "lse", _F32, (R,)) if out.get("lse") is not None else \
-        torch.empty(R, dtype=_F32, device=dev)
+    logp, lse = out.get("logp"), out.get("lse")
+    logp = torch.empty(R, dtype=_F32, device=dev) if logp is None else _is(logp, "logp", _F32, R)
+    lse = torch.empty(R, dtype=_F32, device=dev) if lse is None else _is(lse, "lse", _F32, R)
     st = new_status(dev) if status is None else status
     nbytes = shaping.workspace_bytes
     ws = _caller_workspace(workspace, nbytes) if workspace is not None else WORKSPACE.get(dev, nbytes)
@@ -752,11 +761,11 @@ def grpo_shaped_logp_backward(logits, targets, mask, shaping: Shaping, lse, coef
     or coef 0 are not read and get zeros.  ``dlogits`` may be ``logits`` itself.
     Returns a dict with dlogits and status."""
     dt, ld = _need_logits(logits, "logits", shaping)
-    R = shaping.struct.rows
-    _need(targets, "targets", torch.int32, (R,))
-    _need(mask, "mask", torch.uint8, (R,))
-    _need(lse, "lse", _F32, (R,))
-    _need(coef, "coef", _F32, (R,))
+    R = shaping.rows
+    _is(targets, "targets", torch.int32, R)
+    _is(mask, "mask", torch.uint8, R)
+    _is(lse, "lse", _F32, R)
+    _is(coef, "coef", _F32, R)
     if grad_out is not None:
         _need(grad_out, "grad_out", _F32)
     dev = logits.device
