@@ -55,6 +55,8 @@ constexpr int SH_KEEP = 8;                       // history tokens a thread keep
 constexpr int SH_MAX_ROWS = 32;                  // rows per CTA (one lane each in the set-up)
 constexpr float SH_LOG2E = 1.4426950408889634f;
 constexpr float SH_LOWEST = 3.402823466e38f;     // the largest finite fp32
+constexpr float SH_ONE = 1099511627776.f;          // 2^40: 1 in the sum over the members
+constexpr int SH_FEW = 4;
 constexpr float SH_BIG = 1e37f;                  // beyond this a step to base 2 may overflow
 static_assert(SH_SET % SHAPE_MIN_SEG == 0, "a range of SH_SET columns, which always fits, is whole segments");
 
@@ -305,27 +307,25 @@ __device__ __forceinline__ bool sh_load_row(const ShapeArgs& a, int row, ShRow& 
   return on && coef != 0.f && lse != -INFINITY;
 }
 
-// The ranked set of a range of columns.  `member` and `before` stay as built;
-// `active` has the members whose word is in use by the present row (the others
-// belong to later rows of the chain).
+// The ranked set of a range of columns.  `member`, `before` and `col` stay as
+// built; a member whose word is 0 belongs to later rows of the chain only.
 struct ShSet {
-  uint32_t* member;  // [cols / 32]
-  uint32_t* active;  // [cols / 32]
+  uint32_t* member;  // [cols / 32] a bit per column
   uint32_t* word;    // [SH_SET]
-  uint16_t* before;  // [cols / 32] members before each 32 columns
+  uint16_t* col;     // [SH_SET] a member's column, by rank
+  uint16_t* before;  // [cols / 32 + 1] members before each 32 columns
   __device__ __forceinline__ uint32_t rank(uint32_t j) const {
     return before[j >> 5] + __popc(member[j >> 5] & ((1u << (j & 31)) - 1u));
   }
 };
 
-// one history token, as the k-th of its row
+// one history token of a row
 __device__ __forceinline__ void sh_count(const ShSet& set, uint32_t j, bool prompt) {
   uint32_t* w = set.word + set.rank(j);
   if (prompt)
     atomicOr(w, SH_PROMPT);
   else
     atomicAdd(w, 1u);
-  atomicOr(&set.active[j >> 5], 1u << (j & 31));
 }
 
 // Builds the set of columns [c0, c0 + cols) from the history of `last`, the
@@ -385,9 +385,9 @@ __device__ int sh_build(const ShapeArgs& a, const ShSet& set, const ShRow& first
   if (total > SH_SET) return total;
   for (int i = i0; i < i1; ++i) {
     set.before[i] = static_cast<uint16_t>(off);
-    off += __popc(set.member[i]);
-    set.active[i] = 0;
+    for (uint32_t m = set.member[i]; m; m &= m - 1) set.col[off++] = static_cast<uint16_t>(i * 32 + __ffs(m) - 1);
   }
+  if (tid == 0) set.before[nw] = static_cast<uint16_t>(total);
   for (int i = tid; i < total; i += SH_THREADS) set.word[i] = 0;
   __syncthreads();
   if (first.bias_e > first.bias_b) {  // a chain has one list
@@ -396,7 +396,6 @@ __device__ int sh_build(const ShapeArgs& a, const ShSet& set, const ShRow& first
       if (j < static_cast<uint32_t>(cols)) {
         // the last entry of a token counts
         atomicMax(&set.word[set.rank(j)], static_cast<uint32_t>(k - first.bias_b + 1) << SH_BIAS_SHIFT);
-        atomicOr(&set.active[j >> 5], 1u << (j & 31));
       }
     }
     __syncthreads();
@@ -451,10 +450,10 @@ __global__ void __launch_bounds__(SH_THREADS, OUT_TILE ? 2 : SH_CTAS) shape_kern
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   ShSet set;
   set.member = reinterpret_cast<uint32_t*>(sh_smem);
-  set.active = set.member + a.cols / 32;
-  set.word = set.active + a.cols / 32;
-  set.before = reinterpret_cast<uint16_t*>(set.word + SH_SET);
-  uint8_t* const tiles = reinterpret_cast<uint8_t*>(set.before + a.cols / 32);
+  set.word = set.member + a.cols / 32;
+  set.col = reinterpret_cast<uint16_t*>(set.word + SH_SET);
+  set.before = set.col + SH_SET;
+  uint8_t* const tiles = reinterpret_cast<uint8_t*>(set.before + a.cols / 32 + 8);
   uint8_t* const ring = tiles + warp * (SH_STAGES * SH_TILE);
   uint8_t* const out_tile = tiles + SH_WARPS * (SH_STAGES * SH_TILE) + warp * SH_TILE;
   const int tile = static_cast<int>(blockIdx.x % a.ntiles);
@@ -543,18 +542,18 @@ __global__ void __launch_bounds__(SH_THREADS, OUT_TILE ? 2 : SH_CTAS) shape_kern
       int cols = min(width, t0 + tcols - c0);
       int nseg = (cols + S::COLS - 1) / S::COLS;
       // The copies run SH_STAGES - 1 segments ahead of the present one, the reads
-      // of the allow bits one more: `oks` has them (a byte per chunk) from the
-      // present segment to the one copied next.  `left`: the chain's rows from the
-      // iterator's on.
+      // of the allow bits one more: `oks` has them (lane l those of the segment's
+      // columns 32l .. 32l + 31) from the present segment to the one copied next.
+      // `left`: the chain's rows from the iterator's on.
       uint32_t left_c = 0, oks[SH_STAGES];
       int seg_c = 0, stage_c;
       const uint8_t* src_c = nullptr;    // the segment of the copies' iterator in the logits
-      const uint8_t* allow_c = nullptr;  // its row's allow bits from c0 on, if any
-      const auto row_c = [&] {           // the iterator enters a row
+      const uint32_t* allow_c = nullptr;  // its row's allow bits from c0 on, if any
+      const auto row_c = [&] {            // the iterator enters a row
         const int rr = __ffs(left_c) - 1;
         src_c = first_byte + (static_cast<size_t>(row0 + rr) * a.ld + (c0 + warp * S::COLS)) * sizeof(TIn);
         const int k = MASKS ? rows[rr].allow : -1;
-        allow_c = k < 0 ? nullptr : reinterpret_cast<const uint8_t*>(a.s.allow_bits + k * allow_ld) + (c0 >> 3);
+        allow_c = k < 0 ? nullptr : a.s.allow_bits + k * allow_ld + (c0 >> 5);
         seg_c = warp;
       };
       const auto next_c = [&] {
@@ -566,32 +565,37 @@ __global__ void __launch_bounds__(SH_THREADS, OUT_TILE ? 2 : SH_CTAS) shape_kern
         }
       };
       const auto load_ok = [&] {
-        if ((!MASKS || !allow_c) && (seg_c + 1) * S::COLS <= cols) return S::FULL;
-        if (!left_c) return 0u;
+        if ((!MASKS || !allow_c) && (seg_c + 1) * S::COLS <= cols) return 0xffffffffu;
+        const int w = seg_c * S::WORDS + lane, n = cols - w * 32;
+        if (!left_c || lane >= S::WORDS || n <= 0) return 0u;
+        uint32_t ok = n < 32 ? (1u << n) - 1u : 0xffffffffu;
+        if (MASKS && allow_c) ok &= __ldg(allow_c + w);
+        return ok;
+      };
+      // a lane's eight columns of each chunk as bytes, from a word of 32 columns per lane
+      const auto bytes_of = [&](uint32_t word) {
         uint32_t ok = 0;
-        const int j0 = seg_c * S::COLS + lane * 8;
 #pragma unroll
         for (int u = 0; u < S::CHUNKS; ++u) {
-          const int j = j0 + u * 256, n = cols - j;
-          uint32_t o = n <= 0 ? 0u : (n < 8 ? (1u << n) - 1u : 0xffu);
-          if (MASKS && allow_c && n > 0) o &= __ldg(allow_c + (j >> 3));
-          ok |= o << (8 * u);
+          const uint32_t w = __shfl_sync(0xffffffffu, word, u * 8 + (lane >> 2));
+          ok |= ((w >> ((lane & 3) * 8)) & 0xffu) << (8 * u);
         }
         return ok;
       };
-      // copies a segment's 16-byte words; `ok` is of this lane's columns
-      const auto copy = [&](uint32_t ok, uint8_t* dst) {
+      // copies a segment's 16-byte words
+      const auto copy = [&](uint32_t word, uint8_t* dst) {
         if (left_c) {
           if (ALIGNED) {
             const uint8_t* from = src_c + lane * 16 * S::LANE16;
             uint8_t* to = dst + lane * 16 * S::LANE16;
-            if (ok == S::FULL) {
+            if ((!MASKS || !allow_c) && (seg_c + 1) * S::COLS <= cols) {
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 const int at = (q / S::LANE16) * CB + (q % S::LANE16) * 16;
                 sh_copy16(to + at, from + at, 16);
               }
             } else {
+              const uint32_t ok = bytes_of(word);
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 const int u = q / S::LANE16, at = u * CB + (q % S::LANE16) * 16;
@@ -675,7 +679,7 @@ __global__ void __launch_bounds__(SH_THREADS, OUT_TILE ? 2 : SH_CTAS) shape_kern
         __syncwarp();  // every lane's part has landed, and the stage before is read
         copy(oks[SH_STAGES - 1], ring + stage_c * SH_TILE);
         if (left_c) next_c();
-        const uint32_t ok = oks[0];
+        const uint32_t okw = oks[0];
 #pragma unroll
         for (int k = 0; k < SH_STAGES - 1; ++k) oks[k] = oks[k + 1];
         oks[SH_STAGES - 1] = load_ok();
@@ -688,91 +692,115 @@ __global__ void __launch_bounds__(SH_THREADS, OUT_TILE ? 2 : SH_CTAS) shape_kern
                                         first_byte + (static_cast<size_t>(row) * a.ld + (c0 + seg)) * sizeof(TIn)) & 15);
         TIn* const x = reinterpret_cast<TIn*>(buf + shift);  // the segment's columns
 
-        // the members among this lane's 32 columns, and the target
-        const int w0 = sg * S::WORDS + lane;  // word of the set
-        uint32_t mine = 0, target = 0, allowed = 0xffffffffu;
-        if (ranked && lane < S::WORDS && (whole || w0 * 32 < cols)) mine = set.active[w0];
-        if (MODE != SHAPE_OUT && sg == ysg && (y >> 5) == w0) target = 1u << (y & 31);
-        if (MASKS && (mine | target) && allow >= 0)
-          allowed = __ldg(a.s.allow_bits + allow * allow_ld + ((c0 >> 5) + w0));
-        uint32_t visit = (mine | target) & allowed;
-        const bool sparse = (ranked || sg == ysg) && __any_sync(0xffffffffu, visit != 0);
-        // a member's word, by its bit: ranks follow on the members before this lane's columns
-        uint32_t base = 0, member = 0;
-        if (ranked && visit) {
-          base = set.before[w0];
-          member = set.member[w0];
+        // members of the segment, by rank: a lane each, in as many rounds as it takes
+        int r0 = 0, r1 = 0;
+        if (ranked) {
+          r0 = set.before[sg * S::WORDS];
+          r1 = set.before[min((sg + 1) * S::WORDS, (cols + 31) >> 5)];
         }
-        const auto word_of = [&](uint32_t bit) {
-          return (mine & bit) ? set.word[base + __popc(member & (bit - 1u))] : 0u;
-        };
+        const bool masked = MASKS && allow >= 0;
+        const uint32_t* const allow_row = masked ? a.s.allow_bits + allow * allow_ld + (c0 >> 5) : nullptr;
+        const auto allowed = [&](int j) { return !masked || ((__ldg(allow_row + (j >> 5)) >> (j & 31)) & 1u) != 0; };
+        // a mask that leaves at most SH_FEW of any 32 columns: the sparse way costs less than the dense pass
+        const bool few = masked && __reduce_max_sync(0xffffffffu, __popc(okw)) <= SH_FEW;
 
         if (MODE == SHAPE_LOGP) {
-          if (MASKS && (target & ~allowed)) a.zy[row] = -INFINITY;
-          float ml = -INFINITY, sl = 0.f;
-          if (sparse) {
-            bool more = false;
-            while (visit) {
-              const uint32_t bit = visit & (0u - visit);
-              visit ^= bit;
-              TIn* const p = x + lane * 32 + __ffs(bit) - 1;
+          // members: their values go into a sum of integers (units of 2^-40 of the largest), which does not depend on
+          // the order, as ranks depend on the rows of the chain; their staged places get -inf
+          float zm = -INFINITY, z0 = -INFINITY;
+          unsigned long long fixed = 0;
+          bool mine_is_target = false, nan = false;
+          if (r1 > r0) {
+            const auto value = [&](int q, int& j) {
+              const uint32_t w = set.word[q];
+              j = -1;
+              if (!w) return -INFINITY;
+              j = set.col[q];
               float slope;
-              const float z = sh_member(pen, word_of(bit), sh_to_float<TIn>(*p), slope) * inv_t;
-              if (bit & target) a.zy[row] = z;
-              if (bit & mine) {
-                *p = sh_from_float<TIn>(-INFINITY);
-                if (!more) {
-                  ml = z, sl = 1.f;
-                  more = true;
+              return allowed(j) ? sh_member(pen, w, sh_to_float<TIn>(x[j - seg]), slope) * inv_t : -INFINITY;
+            };
+            int j0 = -1, j;
+            if (r0 + lane < r1) z0 = value(r0 + lane, j0);
+            zm = z0;
+            for (int q = r0 + 32 + lane; q < r1; q += 32) zm = fmaxf(zm, value(q, j));
+            zm = fmaxf(sh_warp_max(zm), -SH_LOWEST);  // the lowest finite value in place of -inf
+            const auto add = [&](float z, int at) {
+              if (at < 0) return;
+              const float e = ex2_approx((z - zm) * SH_LOG2E);
+              nan |= e != e;
+              fixed += static_cast<unsigned long long>(e * SH_ONE);
+              if (at == y) {
+                a.zy[row] = z;
+                mine_is_target = true;
+              }
+              x[at - seg] = sh_from_float<TIn>(-INFINITY);
+            };
+            add(z0, j0);
+            for (int q = r0 + 32 + lane; q < r1; q += 32) {
+              const float z = value(q, j);
+              add(z, j);
+            }
+            mine_is_target = __any_sync(0xffffffffu, mine_is_target);
+            __syncwarp();
+          }
+          if (sg == ysg && !mine_is_target && lane == 0) a.zy[row] = allowed(y) ? sh_to_float<TIn>(x[y - seg]) * inv_t : -INFINITY;
+          float m = -INFINITY, sum = 0.f, ml = -INFINITY, sl = 0.f;
+          ShRaw<TIn> raw[S::CHUNKS];
+          if (few) {
+            for (uint32_t v = okw; v; v &= v - 1) {
+              const float z = sh_to_float<TIn>(x[lane * 32 + __ffs(v) - 1]) * inv_t;
+              const float mn = fmaxf(fmaxf(ml, z), -SH_LOWEST);
+              sl = sl * ex2_approx((ml - mn) * SH_LOG2E) + ex2_approx((z - mn) * SH_LOG2E);
+              ml = mn;
+            }
+            m = ml;
+          } else {
+            if (masked || !whole) {
+              // barred columns to -inf, in the stage
+              const uint32_t ok = bytes_of(okw);
+#pragma unroll
+              for (int u = 0; u < S::CHUNKS; ++u) {
+                const uint32_t bar = ((ok >> (8 * u)) & 0xffu) ^ 0xffu;
+                if (shift == 0) {
+                  sh_read<ShRaw<TIn>::N>(raw[u].w, buf + u * CB + lane * 16 * S::LANE16, 0);
+                  sh_fill(raw[u], bar, sh_minus_inf<TIn>());
+#pragma unroll
+                  for (int q = 0; q < ShRaw<TIn>::N / 4; ++q)
+                    *(reinterpret_cast<uint4*>(buf + u * CB + lane * 16 * S::LANE16) + q) =
+                        make_uint4(raw[u].w[4 * q], raw[u].w[4 * q + 1], raw[u].w[4 * q + 2], raw[u].w[4 * q + 3]);
                 } else {
-                  // the lowest finite value in place of -inf, whose difference with itself is no number
-                  const float mn = fmaxf(fmaxf(ml, z), -SH_LOWEST);
-                  sl = sl * ex2_approx((ml - mn) * SH_LOG2E) + ex2_approx((z - mn) * SH_LOG2E);
-                  ml = mn;
+                  for (uint32_t v = bar; v; v &= v - 1) x[u * 256 + lane * 8 + __ffs(v) - 1] = sh_from_float<TIn>(-INFINITY);
                 }
               }
+              __syncwarp();
             }
-            __syncwarp();
-          }
-          const uint32_t bars = ok ^ S::FULL;
-          if ((MASKS || !whole) && __any_sync(0xffffffffu, bars != 0)) {
-            // barred columns to -inf, in the stage
 #pragma unroll
-            for (int u = 0; u < S::CHUNKS; ++u) {
-              const uint32_t bar = (bars >> (8 * u)) & 0xffu;
+            for (int u = 0; u < S::CHUNKS; ++u) sh_read<ShRaw<TIn>::N>(raw[u].w, buf + u * CB + lane * 16 * S::LANE16, shift);
+            if constexpr (sizeof(TIn) == 2) {
+              __nv_bfloat162 h[S::CHUNKS * 4];
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if ((bar >> e) & 1u) x[u * 256 + lane * 8 + e] = sh_from_float<TIn>(-INFINITY);
+              for (int u = 0; u < S::CHUNKS; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) h[u * 4 + i] = *reinterpret_cast<const __nv_bfloat162*>(&raw[u].w[i]);
+#pragma unroll
+              for (int o = S::CHUNKS * 2; o > 0; o >>= 1)
+#pragma unroll
+                for (int i = 0; i < o; ++i) h[i] = __hmax2(h[i], h[i + o]);
+              m = fmaxf(__low2float(h[0]), __high2float(h[0]));
+            } else {
+#pragma unroll
+              for (int u = 0; u < S::CHUNKS; ++u)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) m = fmaxf(m, __uint_as_float(raw[u].w[i]));
             }
-            __syncwarp();
+            m *= inv_t;  // 1 / T > 0: the maximum of the raw values is that of the scaled ones
           }
-          ShRaw<TIn> raw[S::CHUNKS];
-#pragma unroll
-          for (int u = 0; u < S::CHUNKS; ++u) sh_read<ShRaw<TIn>::N>(raw[u].w, buf + u * CB + lane * 16 * S::LANE16, shift);
-          float m;
-          if constexpr (sizeof(TIn) == 2) {
-            __nv_bfloat162 h[S::CHUNKS * 4];
-#pragma unroll
-            for (int u = 0; u < S::CHUNKS; ++u)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) h[u * 4 + i] = *reinterpret_cast<const __nv_bfloat162*>(&raw[u].w[i]);
-#pragma unroll
-            for (int o = S::CHUNKS * 2; o > 0; o >>= 1)
-#pragma unroll
-              for (int i = 0; i < o; ++i) h[i] = __hmax2(h[i], h[i + o]);
-            m = fmaxf(__low2float(h[0]), __high2float(h[0]));
-          } else {
-            m = -INFINITY;
-#pragma unroll
-            for (int u = 0; u < S::CHUNKS; ++u)
-#pragma unroll
-              for (int i = 0; i < 8; ++i) m = fmaxf(m, __uint_as_float(raw[u].w[i]));
-          }
-          // 1 / T > 0: the maximum of the raw values is that of the scaled ones
-          m = sh_warp_max(fmaxf(m * inv_t, ml));
+          m = fmaxf(sh_warp_max(m), zm);
           const float ref = fmaxf(m, -SH_LOWEST);
-          float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          if (fabsf(ref) < SH_BIG) {
+          if (few) {
+            sum = sl * ex2_approx((ml - ref) * SH_LOG2E);
+          } else if (fabsf(ref) < SH_BIG) {
+            float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             const float k = inv_t * SH_LOG2E, c = -ref * SH_LOG2E;
             const float2 k2 = make_float2(k, k), c2 = make_float2(c, c);
 #pragma unroll
@@ -782,6 +810,7 @@ __global__ void __launch_bounds__(SH_THREADS, OUT_TILE ? 2 : SH_CTAS) shape_kern
                 const float2 v = sh_fma2(sh_pair(raw[u], i), k2, c2);
                 acc[i & 1] = sh_add2(acc[i & 1], make_float2(ex2_approx(v.x), ex2_approx(v.y)));
               }
+            sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
           } else {  // values near the type's lowest: the difference first
 #pragma unroll 1
             for (int u = 0; u < S::CHUNKS; ++u) {
@@ -789,45 +818,55 @@ __global__ void __launch_bounds__(SH_THREADS, OUT_TILE ? 2 : SH_CTAS) shape_kern
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const float2 v = sh_pair(raw[0], i);
-                acc[0].x += ex2_approx(fmaf(v.x, inv_t, -ref) * SH_LOG2E);
-                acc[0].y += ex2_approx(fmaf(v.y, inv_t, -ref) * SH_LOG2E);
+                sum += ex2_approx(fmaf(v.x, inv_t, -ref) * SH_LOG2E);
+                sum += ex2_approx(fmaf(v.y, inv_t, -ref) * SH_LOG2E);
               }
             }
           }
-          float sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-          if (sparse) sum += sl * ex2_approx((ml - ref) * SH_LOG2E);
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          if (r1 > r0) {
+            // at most 1024 members: the high parts add up to below 2^31, the low ones to 2^30
+            const uint32_t hi = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(fixed >> 20));
+            const uint32_t lo = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(fixed) & 0xfffffu);
+            const float t = static_cast<float>((static_cast<unsigned long long>(hi) << 20) + lo) * (1.f / SH_ONE);
+            sum += t * ex2_approx((zm - ref) * SH_LOG2E);
+            if (__any_sync(0xffffffffu, nan)) sum = __int_as_float(0x7fc00000);
+          }
           if (lane == 0) part[sg] = make_float2(m, sum);
         } else {
           TOut* const out = reinterpret_cast<TOut*>(a.out) + static_cast<size_t>(row) * a.out_ld + (c0 + seg);
-          const uint32_t bars = ok ^ S::FULL;
-          const bool barred = MASKS && __any_sync(0xffffffffu, bars != 0);
+          const uint32_t bars = masked ? bytes_of(okw) ^ S::FULL : 0u;
           const bool small = fabsf(lse) < SH_BIG;
           const float k = MODE == SHAPE_OUT ? inv_t : inv_t * SH_LOG2E, c = -lse * SH_LOG2E;
           const float2 k2 = make_float2(k, k), c2 = make_float2(c, c), g2 = make_float2(-scale, -scale);
 #pragma unroll
           for (int u = 0; u < S::CHUNKS; ++u) {
-            ShRaw<TIn> raw;
-            sh_read<ShRaw<TIn>::N>(raw.w, buf + u * CB + lane * 16 * S::LANE16, shift);
             ShRaw<TOut> o;
+            if (few) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float2 v = sh_pair(raw, i);
-              if (MODE == SHAPE_OUT) {
-                v = sh_mul2(v, k2);
-              } else {
-                if (small) {
-                  v = sh_fma2(v, k2, c2);
-                } else {  // the difference first
-                  v.x = fmaf(v.x, inv_t, -lse) * SH_LOG2E;
-                  v.y = fmaf(v.y, inv_t, -lse) * SH_LOG2E;
+              for (int i = 0; i < ShRaw<TOut>::N; ++i) o.w[i] = MODE == SHAPE_OUT ? sh_minus_inf<TOut>() : 0u;
+            } else {
+              ShRaw<TIn> raw;
+              sh_read<ShRaw<TIn>::N>(raw.w, buf + u * CB + lane * 16 * S::LANE16, shift);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float2 v = sh_pair(raw, i);
+                if (MODE == SHAPE_OUT) {
+                  v = sh_mul2(v, k2);
+                } else {
+                  if (small) {
+                    v = sh_fma2(v, k2, c2);
+                  } else {  // the difference first
+                    v.x = fmaf(v.x, inv_t, -lse) * SH_LOG2E;
+                    v.y = fmaf(v.y, inv_t, -lse) * SH_LOG2E;
+                  }
+                  v = sh_mul2(make_float2(ex2_approx(v.x), ex2_approx(v.y)), g2);
                 }
-                v = sh_mul2(make_float2(ex2_approx(v.x), ex2_approx(v.y)), g2);
+                sh_put(o, i, v);
               }
-              sh_put(o, i, v);
+              if (masked) sh_fill(o, (bars >> (8 * u)) & 0xffu, MODE == SHAPE_OUT ? sh_minus_inf<TOut>() : 0u);
             }
-            if (barred) sh_fill(o, (bars >> (8 * u)) & 0xffu, MODE == SHAPE_OUT ? sh_minus_inf<TOut>() : 0u);
             const int j = u * 256 + lane * 8, n = cols - seg - j;
             if (OUT_TILE) {
 #pragma unroll
@@ -848,25 +887,34 @@ __global__ void __launch_bounds__(SH_THREADS, OUT_TILE ? 2 : SH_CTAS) shape_kern
               }
             }
           }
-          if (sparse) {
+          const bool here = MODE == SHAPE_GRAD && sg == ysg;
+          if (few || r1 > r0 || here) {
             __syncwarp();  // after the dense stores of the other lanes
-            while (visit) {
-              const uint32_t bit = visit & (0u - visit);
-              visit ^= bit;
-              const int j = lane * 32 + __ffs(bit) - 1;
+            TOut* const to = OUT_TILE ? reinterpret_cast<TOut*>(out_tile) : out;
+            // column j of the segment with a member's word, or 0
+            const auto put = [&](int j, uint32_t w) {
               float slope;
-              const float z = sh_member(pen, word_of(bit), sh_to_float<TIn>(x[j]), slope);
+              const float z = sh_member(pen, w, sh_to_float<TIn>(x[j]), slope);
               float v;
               if (MODE == SHAPE_OUT) {
                 v = z * inv_t;
               } else {
                 const float p = ex2_approx(fmaf(z, inv_t, -lse) * SH_LOG2E);
-                v = scale * slope * (((bit & target) ? 1.f : 0.f) - p);
+                v = scale * slope * ((j + seg == y ? 1.f : 0.f) - p);
               }
-              if (OUT_TILE)
-                reinterpret_cast<TOut*>(out_tile)[j] = sh_from_float<TOut>(v);
-              else
-                out[j] = sh_from_float<TOut>(v);
+              to[j] = sh_from_float<TOut>(v);
+            };
+            if (few) {
+              for (uint32_t v = okw; v; v &= v - 1) put(lane * 32 + __ffs(v) - 1, 0u);
+              __syncwarp();
+            } else if (here) {
+              if (lane == 0 && allowed(y)) put(y - seg, 0u);
+              __syncwarp();
+            }
+            for (int q = r0 + lane; q < r1; q += 32) {
+              const uint32_t w = set.word[q];
+              const int j = set.col[q];
+              if (w && allowed(j)) put(j - seg, w);
             }
           }
           if (OUT_TILE) {
@@ -888,7 +936,6 @@ __global__ void __launch_bounds__(SH_THREADS, OUT_TILE ? 2 : SH_CTAS) shape_kern
             __syncwarp();  // the output tile is free
           }
         }
-
       }
       }
       sh_copy_wait<0>();
@@ -948,7 +995,7 @@ __global__ void __launch_bounds__(256) shaped_merge_kernel(const ShapeArgs a) {
 template <class TIn, class TOut, int MODE, bool ALIGNED, bool OUT_TILE, bool MASKS>
 cudaError_t launch_typed(const ShapeArgs& a, cudaStream_t st) {
   const auto bytes = [](size_t cols) {
-    return cols / 32 * 10 + SH_SET * 4 + SH_WARPS * (SH_STAGES + (OUT_TILE ? 1 : 0)) * SH_TILE;
+    return cols / 32 * 6 + 16 + SH_SET * 6 + SH_WARPS * (SH_STAGES + (OUT_TILE ? 1 : 0)) * SH_TILE;
   };
   const auto kernel = shape_kernel<TIn, TOut, MODE, ALIGNED, OUT_TILE, MASKS>;
   static std::atomic<uint64_t> ready{0};  // a bit per device whose limit is set
