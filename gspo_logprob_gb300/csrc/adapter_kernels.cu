@@ -1,9 +1,10 @@
 // Logits of a shared head with low-rank adapters, one per row:
 //   z_i = W h_i + s_a B_a (A_a h_i),   a = adapter_id[i] (or none).
 //
-// bf16: two launches.  The first forms u_i = s_a A_a h_i (fp32 sums) and lays it
-// out for the tensor cores; the second is one tcgen05 product whose K runs over
-// the hidden size and then over 16-wide chunks of the adapters in use:
+// bf16: u_i = s_a A_a h_i (fp32 sums) is formed and laid out for the tensor cores,
+// by the product itself in decode calls and by a launch before it otherwise; the
+// product is one tcgen05 pass whose K runs over the hidden size and then over
+// 16-wide chunks of the adapters in use:
 //   Z = H W^T + sum_a U_a B_a^T,   U_a = u_i in the rows of adapter a, else 0.
 // The rows of a tile need not be sorted by adapter, the low-rank part costs a
 // pass over the B_a in use and nothing is added to the logits afterwards.  Decode
@@ -28,38 +29,44 @@ namespace {
 
 // ---------------------------------------------------------------- u = s A h
 constexpr int AD_THREADS = 256;
-constexpr int AD_RANKS = 8;  // ranks per CTA: one per warp
 
-// acc + the dot product of eight bf16 pairs
-__device__ __forceinline__ float ad_dot8(const uint4& x, const uint4& y, float acc) {
+// acc + the dot product of eight bf16 pairs, even and odd places apart (two
+// columns per instruction).  Every path adds a row's terms in this order.
+__device__ __forceinline__ float2 ad_dot8(const uint4& x, const uint4& y, float2 acc) {
   const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    acc = fmaf(__uint_as_float(xw[i] << 16), __uint_as_float(yw[i] << 16), acc);
-    acc = fmaf(__uint_as_float(xw[i] & 0xffff0000u), __uint_as_float(yw[i] & 0xffff0000u), acc);
+    asm("{\n\t.reg .b64 ra, rb, rc;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%0, %1};\n\t"
+        "fma.rn.f32x2 rc, ra, rb, rc;\n\tmov.b64 {%0, %1}, rc;\n\t}"
+        : "+f"(acc.x), "+f"(acc.y)
+        : "f"(__uint_as_float(xw[i] << 16)), "f"(__uint_as_float(xw[i] & 0xffff0000u)),
+          "f"(__uint_as_float(yw[i] << 16)), "f"(__uint_as_float(yw[i] & 0xffff0000u)));
   }
   return acc;
 }
+__device__ __forceinline__ uint4 ad_load8(const __nv_bfloat16* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 
-// One CTA: RPC consecutive rows (of one row tile) times 8 ranks.  It finds the
-// adapters of the row tile in the order of their first rows (the tile's slots),
-// and writes its rows' part of every slot's chunk: u in their own slot, 0 in the
-// others.  U: [tiles, max_chunks, high/low, tile rows, 16] bf16; list: per tile
-// the number of slots, then each slot's adapter.
-// RPC = 1 for decode (latency: one dot per warp), 8 for prompts (a row of A_a is
-// read once for eight rows of the same request).
-template <int RPC>
+// One CTA: RPC consecutive rows (of one row tile) times 8 RPW ranks, RPW of them
+// per warp.  It finds the adapters of the row tile in the order of their first
+// rows (the tile's slots), and writes its rows' part of every slot's chunks: u in
+// their own slot, 0 in the others.  U: [tiles, max_chunks, high/low, tile rows,
+// 16] bf16; list: per tile the number of slots, then each slot's adapter.
+// <1, 1> up to 1023 rows (one dot per warp), <8, 4> for prompts: the rows of a
+// request share a read of A_a, the ranks of a warp one of the rows (2048 rows,
+// rank 32, D = 4096: MEASURED_LOW us, against 170 with a dot at a time).
+template <int RPC, int RPW>
 __global__ void __launch_bounds__(AD_THREADS) adapter_low_kernel(const AdapterArgs a) {
+  constexpr int RANKS = AD_THREADS / 32 * RPW;
   __shared__ int ids[256];
   __shared__ int first[256];  // first row of the tile with the same adapter
   __shared__ int slot_of[256];
   __shared__ int warp_n[AD_THREADS / 32];
-  __shared__ float u[RPC][AD_RANKS];
+  __shared__ float u[RPC][RANKS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int row0 = blockIdx.x * RPC;
   const int tile = row0 / a.tile_rows, base = tile * a.tile_rows;
-  const int j = blockIdx.y * AD_RANKS + warp;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product may start beside this launch
+  const int j0 = blockIdx.y * RANKS + warp * RPW;
 
   int id = -1;
   if (tid < a.tile_rows && base + tid < a.N) {
@@ -72,63 +79,68 @@ __global__ void __launch_bounds__(AD_THREADS) adapter_low_kernel(const AdapterAr
   ids[tid] = id;
   __syncthreads();
   // the dot products need the rows' adapters only
-  float acc[RPC];
+  float2 acc[RPC][RPW];
 #pragma unroll
-  for (int q = 0; q < RPC; ++q) acc[q] = 0.f;
-  if (j < a.rank) {
-    int rid[RPC];
-    bool any = false;
+  for (int q = 0; q < RPC; ++q)
 #pragma unroll
-    for (int q = 0; q < RPC; ++q) {
-      rid[q] = ids[row0 - base + q];
-      any |= rid[q] >= 0;
+    for (int t = 0; t < RPW; ++t) acc[q][t] = make_float2(0.f, 0.f);
+  const size_t astep = static_cast<size_t>(a.rank) * a.D;
+  const __nv_bfloat16* A0 = static_cast<const __nv_bfloat16*>(a.A) + static_cast<size_t>(j0) * a.D;
+  const __nv_bfloat16* H0 = static_cast<const __nv_bfloat16*>(a.H) + static_cast<size_t>(row0) * a.D;
+  const int nt = min(RPW, a.rank - j0);  // ranks of this warp that exist
+  const int id0 = ids[row0 - base];
+  bool one = id0 >= 0 && nt == RPW;  // the rows have one adapter
+#pragma unroll
+  for (int q = 1; q < RPC; ++q) one &= ids[row0 - base + q] == id0;
+  if (one) {
+    const __nv_bfloat16* A1 = A0 + id0 * astep;
+#pragma unroll(RPC == 1 ? 4 : 1)
+    for (int k = lane * 8; k < a.D; k += 256) {
+      uint4 w[RPW], h[RPC];
+#pragma unroll
+      for (int t = 0; t < RPW; ++t) w[t] = ad_load8(A1 + static_cast<size_t>(t) * a.D + k);
+#pragma unroll
+      for (int q = 0; q < RPC; ++q) h[q] = ad_load8(H0 + static_cast<size_t>(q) * a.D + k);
+#pragma unroll
+      for (int q = 0; q < RPC; ++q)
+#pragma unroll
+        for (int t = 0; t < RPW; ++t) acc[q][t] = ad_dot8(w[t], h[q], acc[q][t]);
     }
-    if (any) {
-      const size_t astep = static_cast<size_t>(a.rank) * a.D;
-      const __nv_bfloat16* A0 = static_cast<const __nv_bfloat16*>(a.A) + static_cast<size_t>(j) * a.D;
-      const __nv_bfloat16* H0 = static_cast<const __nv_bfloat16*>(a.H) + static_cast<size_t>(row0) * a.D;
-      bool one = true;  // the rows have one adapter: its row of A is read once for all of them
-#pragma unroll
-      for (int q = 1; q < RPC; ++q) one &= rid[q] == rid[0];
-      if (one) {
-        const __nv_bfloat16* A1 = A0 + rid[0] * astep;
-#pragma unroll 2
-        for (int k = lane * 8; k < a.D; k += 256) {
-          const uint4 w = __ldg(reinterpret_cast<const uint4*>(A1 + k));
-          uint4 h[RPC];
-#pragma unroll
-          for (int q = 0; q < RPC; ++q) h[q] = __ldg(reinterpret_cast<const uint4*>(H0 + static_cast<size_t>(q) * a.D + k));
-#pragma unroll
-          for (int q = 0; q < RPC; ++q) acc[q] = ad_dot8(w, h[q], acc[q]);
-        }
-      } else {
+  } else if (nt > 0) {
+    // runs of rows with one adapter
+    for (int q0 = 0, q1; q0 < RPC; q0 = q1) {
+      const int i = ids[row0 - base + q0];
+      for (q1 = q0 + 1; q1 < RPC && ids[row0 - base + q1] == i; ++q1) {
+      }
+      if (i < 0) continue;
+      const __nv_bfloat16* A1 = A0 + i * astep;
 #pragma unroll 1
-        for (int q = 0; q < RPC; ++q) {
-          float s = 0.f;
-          const int i = ids[row0 - base + q];
-          if (i >= 0) {
-#pragma unroll 4
-            for (int k = lane * 8; k < a.D; k += 256)
-              s = ad_dot8(__ldg(reinterpret_cast<const uint4*>(A0 + i * astep + k)),
-                          __ldg(reinterpret_cast<const uint4*>(H0 + static_cast<size_t>(q) * a.D + k)), s);
+      for (int k = lane * 8; k < a.D; k += 256) {
+        uint4 w[RPW], h[RPC];
+#pragma unroll
+        for (int t = 0; t < RPW; ++t) w[t] = ad_load8(A1 + static_cast<size_t>(min(t, nt - 1)) * a.D + k);
+#pragma unroll
+        for (int q = 0; q < RPC; ++q) h[q] = ad_load8(H0 + static_cast<size_t>(min(max(q, q0), q1 - 1)) * a.D + k);
+#pragma unroll
+        for (int q = 0; q < RPC; ++q)
+          if (q >= q0 && q < q1) {
+#pragma unroll
+            for (int t = 0; t < RPW; ++t) acc[q][t] = ad_dot8(w[t], h[q], acc[q][t]);
           }
-#pragma unroll
-          for (int t = 0; t < RPC; ++t) acc[t] = t == q ? s : acc[t];
-        }
-      }
-#pragma unroll
-      for (int q = 0; q < RPC; ++q) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) acc[q] += __shfl_xor_sync(0xffffffffu, acc[q], o);
       }
     }
-    if (lane == 0) {
+  }
 #pragma unroll
-      for (int q = 0; q < RPC; ++q) u[q][warp] = rid[q] < 0 ? 0.f : acc[q] * a.scale[rid[q]];
+  for (int q = 0; q < RPC; ++q) {
+    const int i = ids[row0 - base + q];
+    const float scale = i < 0 ? 0.f : __ldg(a.scale + i);
+#pragma unroll
+    for (int t = 0; t < RPW; ++t) {
+      float s = acc[q][t].x + acc[q][t].y;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (lane == 0) u[q][warp * RPW + t] = i < 0 || t >= nt ? 0.f : s * scale;
     }
-  } else if (lane == 0) {
-#pragma unroll
-    for (int q = 0; q < RPC; ++q) u[q][warp] = 0.f;
   }
   // slots
   int f = tid;
@@ -154,18 +166,19 @@ __global__ void __launch_bounds__(AD_THREADS) adapter_low_kernel(const AdapterAr
   if (lead && row0 == base && blockIdx.y == 0) a.list[static_cast<size_t>(tile) * a.list_ld + 1 + off] = id;
   if (tid == 0 && row0 == base && blockIdx.y == 0) a.list[static_cast<size_t>(tile) * a.list_ld] = slots;
   __syncthreads();
-  // this CTA's half (8 ranks) of one chunk of every slot
-  const int rc = a.rank_chunks, chunk = blockIdx.y >> 1, half = blockIdx.y & 1;
+  // this CTA's ranks, eight (half a chunk) at a time, in every slot
+  const int rc = a.rank_chunks;
   uint4* U = static_cast<uint4*>(a.U);
-  for (int i = tid; i < slots * RPC * 2; i += AD_THREADS) {
-    const int hl = i & 1, q = (i >> 1) % RPC, s = (i >> 1) / RPC;
+  for (int i = tid; i < slots * RPC * RPW * 2; i += AD_THREADS) {
+    const int hl = i & 1, g = (i >> 1) % RPW, q = (i >> 1) / RPW % RPC, s = (i >> 1) / (RPW * RPC);
+    const int eight = blockIdx.y * RPW + g, chunk = eight >> 1, half = eight & 1;
     const int row = row0 + q - base;
-    if (base + row >= a.N) continue;
+    if (base + row >= a.N || chunk >= rc) continue;
     uint32_t w[4] = {0, 0, 0, 0};
     if (ids[row] >= 0 && slot_of[first[row]] == s) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float x = u[q][2 * e], y = u[q][2 * e + 1];
+        float x = u[q][8 * g + 2 * e], y = u[q][8 * g + 2 * e + 1];
         if (hl) {  // what the rounding to the high term left
           x -= __bfloat162float(__float2bfloat16_rn(x));
           y -= __bfloat162float(__float2bfloat16_rn(y));
@@ -236,8 +249,72 @@ struct AdCfg {
   static constexpr int TURN_BYTES = 32 * TURN_LD * 4;
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_WARPS * TURN_BYTES + 1024 + 512;
   static_assert(CHUNKS * CHUNK_BYTES <= STAGE_BYTES, "chunks share the stages");
-  static_assert((2 * STAGES + 2 * NUM_ACC + 1) * 8 + 8 <= 512, "barriers");
+  static_assert((2 * STAGES + 2 * NUM_ACC + 2) * 8 + 8 <= 512, "barriers");
 };
+
+// Waits until *counter reads `all`, at most timeout_ns (or until the CTA's abort
+// flag is up).
+__device__ __forceinline__ bool count_wait_bounded(const int* counter, int all, volatile int* abort, int* status,
+                                                   uint64_t timeout_ns) {
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
+    if (v >= all) return true;
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > timeout_ns) {
+      *abort = 1;
+      atomicOr(status, GH_DEV_TIMEOUT);
+      return false;
+    }
+    __nanosleep(64);
+  }
+}
+
+// One row, eight ranks: u by a warp, and the row's part of those ranks' half chunk
+// in every slot.
+__device__ __forceinline__ void ad_item(const AdapterArgs& a, int row, int eight, int id, int slot, int slots, int lane) {
+  float2 acc[8];
+#pragma unroll
+  for (int t = 0; t < 8; ++t) acc[t] = make_float2(0.f, 0.f);
+  const int j0 = eight * 8;
+  const bool on = id >= 0 && j0 < a.rank;  // ranks come in eights
+  if (on) {
+    const __nv_bfloat16* A = static_cast<const __nv_bfloat16*>(a.A) + (static_cast<size_t>(id) * a.rank + j0) * a.D;
+    const __nv_bfloat16* h = static_cast<const __nv_bfloat16*>(a.H) + static_cast<size_t>(row) * a.D;
+#pragma unroll 2
+    for (int k = lane * 8; k < a.D; k += 256) {
+      const uint4 x = ad_load8(h + k);
+#pragma unroll
+      for (int t = 0; t < 8; ++t) acc[t] = ad_dot8(ad_load8(A + static_cast<size_t>(t) * a.D + k), x, acc[t]);
+    }
+  }
+  const float scale = on ? __ldg(a.scale + id) : 0.f;
+  uint32_t hi[4], lo[4];
+#pragma unroll
+  for (int t = 0; t < 8; t += 2) {
+    float v[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      v[e] = acc[t + e].x + acc[t + e].y;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v[e] += __shfl_xor_sync(0xffffffffu, v[e], o);
+      v[e] = on ? v[e] * scale : 0.f;
+    }
+    __nv_bfloat162 p = __floats2bfloat162_rn(v[0], v[1]);
+    hi[t / 2] = *reinterpret_cast<const uint32_t*>(&p);
+    p = __floats2bfloat162_rn(v[0] - __low2float(p), v[1] - __high2float(p));
+    lo[t / 2] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  uint4* U = static_cast<uint4*>(a.U);
+  for (int s = lane; s < 2 * slots; s += 32) {
+    const int hl = s & 1, at_slot = s >> 1;
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (id >= 0 && at_slot == slot) w = hl ? make_uint4(lo[0], lo[1], lo[2], lo[3]) : make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    const size_t r = (static_cast<size_t>(at_slot * a.rank_chunks + (eight >> 1)) * 2 + hl) * a.tile_rows + row;
+    U[r * 2 + (eight & 1)] = w;
+  }
+}
 
 // 32 columns of a row per thread to the output; rows of a warp are consecutive.
 template <class TOut>
@@ -285,11 +362,16 @@ __device__ __forceinline__ void ad_store(const AdapterArgs& a, const float* v, i
   }
 }
 
+// The single-CTA form computes u itself: while the first W tiles stream in, the
+// epilogue warps of all CTAs share the (row, eight ranks) dots, write their part
+// of U and count themselves on a word of the workspace, for which each producer
+// waits before its first chunk (a cooperative launch, so that all CTAs run at
+// once; the wait is bounded like the others).  Each CTA finds the slots itself.
 template <bool PAIR, bool EXACT, class TOut>
 __global__ void __launch_bounds__(AdCfg<PAIR, EXACT>::THREADS, 1)
     adapter_tc_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CUtensorMap tmW,
                       const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmB, const TcSched sc,
-                      const int bn, const AdapterArgs a, const uint64_t timeout_ns) {
+                      const int bn, const int a_rows, const AdapterArgs a, const uint64_t timeout_ns) {
   using C = AdCfg<PAIR, EXACT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -299,9 +381,15 @@ __global__ void __launch_bounds__(AdCfg<PAIR, EXACT>::THREADS, 1)
   uint64_t* tfull = empty + C::STAGES;
   uint64_t* tempty = tfull + C::NUM_ACC;
   uint64_t* drain = tempty + C::NUM_ACC;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
+  __shared__ int ids_s[PAIR ? 1 : TC_BM];    // each row's adapter
+  __shared__ int first_s[PAIR ? 1 : TC_BM];  // the first row with it
+  __shared__ int slot_s[PAIR ? 1 : TC_BM];   // that row's slot
+  __shared__ int list_s[PAIR ? 1 : TC_BM + 1];
+  __shared__ int count_s[C::EPI_WARPS];
+  uint64_t* listed = drain + 1;  // single-CTA form: the slots are in list_s
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0;  // the even CTA of a pair issues its MMAs
   const int cid = PAIR ? blockIdx.x >> 1 : blockIdx.x, ncl = PAIR ? gridDim.x >> 1 : gridDim.x;
@@ -315,6 +403,7 @@ __global__ void __launch_bounds__(AdCfg<PAIR, EXACT>::THREADS, 1)
       mbar_init(&tempty[b], (PAIR ? 2 : 1) * C::EPI_WARPS);
     }
     mbar_init(drain, 1);
+    mbar_init(listed, C::EPI_WARPS);
     *abort_flag = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
@@ -347,7 +436,7 @@ __global__ void __launch_bounds__(AdCfg<PAIR, EXACT>::THREADS, 1)
       int stage = 0;
       uint32_t phase = 0;
       uint32_t pending = 0, pend_par = 0;  // per stage: load issued and its phase parity
-      bool ok = true, issued = false, waited = false;
+      bool ok = true, issued = false, ready = false;
       const auto open_stage = [&](uint32_t bytes) {
         if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, a.status, GH_DEV_TIMEOUT, timeout_ns)) {
           ok = false;
@@ -388,22 +477,24 @@ __global__ void __launch_bounds__(AdCfg<PAIR, EXACT>::THREADS, 1)
         const int n0 = n_blk * bn + static_cast<int>(rank) * C::B_ROWS;
         const int b_rows = PAIR ? C::B_ROWS : bn;
         for (int kb = 0; kb < sc.num_kb; ++kb) {
-          if (!open_stage(C::A_BYTES + b_rows * TC_BK * 2)) break;
+          if (!open_stage((a_rows + b_rows) * TC_BK * 2)) break;
           uint8_t* s = smem + stage * C::STAGE_BYTES;
           load2(s, &tmH, kb * TC_BK, m0);
           load2(s + C::A_BYTES, &tmW, kb * TC_BK, n0);
           close_stage();
         }
-        if (!waited) {
-          // u and the lists are the launch's before; u is read by the asynchronous proxy
-          asm volatile("griddepcontrol.wait;\n\tfence.proxy.async;" ::: "memory");
-          waited = true;
+        const int* list = PAIR ? a.list + static_cast<size_t>(m_blk) * a.list_ld : list_s;
+        if (!PAIR && ok && !ready) {
+          // u is complete when every epilogue warp of the grid has counted itself
+          ok = mbar_wait_bounded(listed, 0, abort_flag, a.status, GH_DEV_TIMEOUT, timeout_ns) &&
+               count_wait_bounded(a.counter, C::EPI_WARPS * gridDim.x, abort_flag, a.status, timeout_ns);
+          asm volatile("fence.proxy.async;" ::: "memory");  // u is read by the asynchronous proxy
+          ready = true;
         }
-        const int* list = a.list + static_cast<size_t>(m_blk) * a.list_ld;
-        const int chunks = ok ? list[0] * rc : 0;
+        const int chunks = ok ? min(max(list[0] * rc, 0), a.max_chunks) : 0;
         for (int c0 = 0; ok && c0 < chunks; c0 += C::CHUNKS) {
           const int n = min(C::CHUNKS, chunks - c0);
-          if (!open_stage(n * (2 * C::U_BYTES + b_rows * 32))) break;
+          if (!open_stage(n * (2 * a_rows + b_rows) * 32)) break;
           for (int q = 0; q < n; ++q) {
             uint8_t* s = smem + stage * C::STAGE_BYTES + q * C::CHUNK_BYTES;
             const int c = c0 + q;
@@ -415,8 +506,6 @@ __global__ void __launch_bounds__(AdCfg<PAIR, EXACT>::THREADS, 1)
           close_stage();
         }
       }
-      // this launch is not over before the one that it depends on
-      if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
       if (!ok) {
         if (PAIR) {
           // completions land on the even CTA's barriers, which this CTA cannot
@@ -441,7 +530,7 @@ __global__ void __launch_bounds__(AdCfg<PAIR, EXACT>::THREADS, 1)
       uint32_t phase = 0;
       int acc = 0;
       uint32_t acc_phase = 0;
-      bool ok = true, issued = false, waited = false;
+      bool ok = true, issued = false, ready = false;
       const auto wait_stage = [&] {
         if (!mbar_wait_bounded(&full[stage], phase, abort_flag, a.status, GH_DEV_TIMEOUT, timeout_ns)) {
           ok = false;
@@ -504,11 +593,12 @@ __global__ void __launch_bounds__(AdCfg<PAIR, EXACT>::THREADS, 1)
           free_stage();
         }
         // the adapters, in the last accumulator
-        if (!waited) {
-          asm volatile("griddepcontrol.wait;" ::: "memory");
-          waited = true;
+        if (!PAIR && ok && !ready) {
+          ok = mbar_wait_bounded(listed, 0, abort_flag, a.status, GH_DEV_TIMEOUT, timeout_ns);
+          ready = true;
         }
-        const int chunks = ok ? a.list[static_cast<size_t>(m_blk) * a.list_ld] * rc : 0;
+        const int* list = PAIR ? a.list + static_cast<size_t>(m_blk) * a.list_ld : list_s;
+        const int chunks = ok ? min(max(list[0] * rc, 0), a.max_chunks) : 0;
         for (int c0 = 0; ok && c0 < chunks; c0 += C::CHUNKS) {
           if (!wait_stage()) break;
           const int n = min(C::CHUNKS, chunks - c0);
@@ -538,6 +628,48 @@ __global__ void __launch_bounds__(AdCfg<PAIR, EXACT>::THREADS, 1)
     const int sub = warp & 3;  // TMEM lane quarter this warp may access
     const uint32_t lane_addr = static_cast<uint32_t>(sub * 32) << 16;
     float* turn = turn_all + (warp - 2) * (C::TURN_BYTES / 4);
+    if constexpr (!PAIR) {
+      static_assert(C::EPI_WARPS * 32 == TC_BM, "a thread per row");
+      const int et = threadIdx.x - 64, ew = warp - 2;
+      const auto sync_epilogue = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+      int id = et < a.N ? a.ids[et] : -1;
+      if (id < -1 || id >= a.num_adapters) {
+        if (blockIdx.x == 0) atomicOr(a.status, GH_DEV_BAD_ROW);
+        id = -1;
+      }
+      ids_s[et] = id;
+      sync_epilogue();
+      int f = et;
+      if (id >= 0) {
+        for (int t = 0; t < et; ++t)
+          if (ids_s[t] == id) {
+            f = t;
+            break;
+          }
+      }
+      const bool lead = id >= 0 && f == et;
+      first_s[et] = f;
+      const uint32_t leads = __ballot_sync(0xffffffffu, lead);
+      if (lane == 0) count_s[ew] = __popc(leads);
+      sync_epilogue();
+      int off = __popc(leads & ((1u << lane) - 1u)), slots = 0;
+      for (int w = 0; w < C::EPI_WARPS; ++w) {
+        if (w < ew) off += count_s[w];
+        slots += count_s[w];
+      }
+      slot_s[et] = off;
+      if (lead) list_s[1 + off] = id;
+      if (et == 0) list_s[0] = slots;
+      sync_epilogue();
+      if (lane == 0) mbar_arrive(listed);
+      const int eights = 2 * rc;
+      for (int item = blockIdx.x * C::EPI_WARPS + ew; item < a.N * eights; item += gridDim.x * C::EPI_WARPS)
+        ad_item(a, item / eights, item % eights, ids_s[item / eights], slot_s[first_s[item / eights]], slots, lane);
+      asm volatile("fence.proxy.async;" ::: "memory");
+      __threadfence();
+      __syncwarp();
+      if (lane == 0) atomicAdd(a.counter, 1);
+    }
     int acc = 0;
     uint32_t acc_phase = 0;
     const auto free_acc = [&] {
@@ -768,13 +900,16 @@ cudaError_t launch_product(const AdapterArgs& a, cudaStream_t st) {
   const int pairs_fit = setup.pairs[this_device()];
   const int bn = PAIR ? C::BN : decode_cols(a.N, a.V, C::BN);
   const uint32_t b_rows = PAIR ? C::B_ROWS : bn;
+  // decode: only the rows that there are, in whole swizzle groups, are loaded; the tile's other rows multiply what
+  // shared memory holds into accumulator rows that nobody reads
+  const uint32_t a_rows = PAIR ? TC_BM : static_cast<uint32_t>(ceil_div(a.N, 8) * 8);
   CUtensorMap th, tw, tu, tb;
   const uint64_t row_bytes = static_cast<uint64_t>(a.D) * 2;
   const int tiles = static_cast<int>(ceil_div(a.N, a.tile_rows));
   const uint64_t u_rows = static_cast<uint64_t>(tiles) * a.max_chunks * 2 * a.tile_rows;
-  if (!make_tmap_bf16(&th, a.H, a.D, a.N, row_bytes, TC_BK, TC_BM) ||
+  if (!make_tmap_bf16(&th, a.H, a.D, a.N, row_bytes, TC_BK, a_rows) ||
       !make_tmap_bf16(&tw, a.W, a.D, a.V, row_bytes, TC_BK, b_rows) ||
-      !make_tmap_bf16_k16(&tu, a.U, 16, u_rows, 1, 32, u_rows * 32, TC_BM) ||
+      !make_tmap_bf16_k16(&tu, a.U, 16, u_rows, 1, 32, u_rows * 32, a_rows) ||
       !make_tmap_bf16_k16(&tb, a.B, a.rank, a.V, a.num_adapters, static_cast<uint64_t>(a.rank) * 2,
                           static_cast<uint64_t>(a.V) * a.rank * 2, b_rows))
     return cudaErrorInvalidValue;
@@ -794,17 +929,25 @@ cudaError_t launch_product(const AdapterArgs& a, cudaStream_t st) {
   cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM_BYTES;
   cfg.stream = st;
-  // the product starts while u is computed and waits for it at its first chunk
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[1];
+  if (PAIR) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+  } else {
+    // CTAs without a tile help with u
+    const int64_t share = ceil_div(static_cast<int64_t>(a.N) * 2 * a.rank_chunks, C::EPI_WARPS);
+    const int helped = static_cast<int>(share < most ? share : most);
+    if (static_cast<int>(cfg.gridDim.x) < helped) cfg.gridDim.x = helped;
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    e = cudaMemsetAsync(a.counter, 0, sizeof(int), st);
+    if (e != cudaSuccess) return e;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = PAIR ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, kern, th, tw, tu, tb, sc, bn, a, timeout_ns());
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, th, tw, tu, tb, sc, bn, static_cast<int>(a_rows), a, timeout_ns());
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
@@ -822,31 +965,23 @@ AdapterPlan adapter_plan(int64_t N, int64_t rank, int64_t num_adapters) {
   const int64_t tiles = ceil_div(N, p.tile_rows);
   p.u_rows = tiles * p.max_chunks * 2 * p.tile_rows;
   p.u_bytes = align_up(static_cast<size_t>(p.u_rows) * 32, 256);
-  p.list_bytes = align_up(static_cast<size_t>(tiles) * p.list_ld * 4, 256);
+  p.list_bytes = align_up(static_cast<size_t>(tiles) * p.list_ld * 4, 256);  // or the counter, with one row tile
   return p;
 }
+
+bool adapter_low_apart(const AdapterArgs& a) { return a.dtype == GH_FP32 || a.tile_rows != TC_BM; }
 
 cudaError_t launch_adapter_low(const AdapterArgs& a, cudaStream_t st) {
   if (a.dtype == GH_FP32) {
     const int64_t warps = static_cast<int64_t>(a.N) * a.rank;
     adapter_low_f32_kernel<<<static_cast<unsigned>(ceil_div(warps, 8)), 256, 0, st>>>(a);
   } else {
-    // Both forms ask for the shared memory split of the product: an SM has to be idle to change its split, and the
-    // product could not start beside this launch.
-    static AdSetup setup;
-    cudaError_t e = once_per_device(setup, [] {
-      cudaError_t r = cudaFuncSetAttribute(adapter_low_kernel<1>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                           cudaSharedmemCarveoutMaxShared);
-      return r != cudaSuccess ? r
-                              : cudaFuncSetAttribute(adapter_low_kernel<8>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                                     cudaSharedmemCarveoutMaxShared);
-    });
-    if (e != cudaSuccess) return e;
-    const unsigned y = static_cast<unsigned>(2 * a.rank_chunks);
+    const int eights = 2 * a.rank_chunks;
     if (a.N < 1024)
-      adapter_low_kernel<1><<<dim3(a.N, y), AD_THREADS, 0, st>>>(a);
+      adapter_low_kernel<1, 1><<<dim3(a.N, eights), AD_THREADS, 0, st>>>(a);
     else
-      adapter_low_kernel<8><<<dim3(static_cast<unsigned>(ceil_div(a.N, 8)), y), AD_THREADS, 0, st>>>(a);
+      adapter_low_kernel<8, 4><<<dim3(static_cast<unsigned>(ceil_div(a.N, 8)), static_cast<unsigned>(ceil_div(eights, 4))),
+                                 AD_THREADS, 0, st>>>(a);
   }
   return cudaGetLastError();
 }

@@ -1008,13 +1008,17 @@ gh_status grpo_adapter_logits(const gh_adapter* p, int32_t* status, void* ws, si
   a.vec_out = aligned16(p->logits) && p->ld * elt % 16 == 0;
   a.U = ws;
   a.list = bf16 ? reinterpret_cast<int32_t*>(static_cast<char*>(ws) + q.u_bytes) : nullptr;
+  a.counter = a.list;  // the product that counts keeps no list in the workspace
   a.tile_rows = q.tile_rows;
   a.rank_chunks = q.rank_chunks;
   a.max_chunks = q.max_chunks;
   a.list_ld = q.list_ld;
   a.status = status;
-  cudaError_t e = run(K_ADAPTER_LOW, st, [&] { return launch_adapter_low(a, st); });
-  if (e != cudaSuccess) return cuda_fail(e, "adapter low-rank launch");
+  cudaError_t e = cudaSuccess;
+  if (adapter_low_apart(a)) {
+    e = run(K_ADAPTER_LOW, st, [&] { return launch_adapter_low(a, st); });
+    if (e != cudaSuccess) return cuda_fail(e, "adapter low-rank launch");
+  }
   e = run(K_ADAPTER_TC, st, [&] { return launch_adapter_logits(a, st); });
   if (e != cudaSuccess) return cuda_fail(e, "adapter logits launch");
   return GH_OK;

@@ -313,9 +313,12 @@ struct AdapterArgs {
   bool vec_out;  // output rows start on 16-byte boundaries
   void* U;       // bf16 [u_rows, 16], or fp32 [N, rank]
   int32_t* list;
+  int* counter;  // bf16, one row tile: the warps of the launch that have written their part of U
   int tile_rows, rank_chunks, max_chunks, list_ld;
   int* status;
 };
+// u, unless the product computes it itself (bf16, one row tile)
+bool adapter_low_apart(const AdapterArgs& a);
 cudaError_t launch_adapter_low(const AdapterArgs& a, cudaStream_t st);
 cudaError_t launch_adapter_logits(const AdapterArgs& a, cudaStream_t st);
 

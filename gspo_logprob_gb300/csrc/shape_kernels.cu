@@ -1036,8 +1036,9 @@ cudaError_t launch_mode(const ShapeArgs& a, cudaStream_t st) {
 // warp and about as much as four more for the rows' parameters and sets; the
 // number of column ranges with the least rounds times cost is taken.  256 rows of
 // 151936 columns: 4 ranges are 2 rounds and 54 us, 5 are 3 rounds and
-// 61 us.  Then as many rows per CTA as leave four rounds (chains get
-// longer; 8 rounds are within 1%).
+// 61 us.  Then as many rows per CTA as leave eight rounds: longer chains save set
+// builds, shorter ones even out rows that are not live (8192 rows of packed
+// sequences: 262 us with 4 rounds, 244 with 8, 261 with 16).
 void plan(ShapeArgs& a) {
   const int64_t slots = static_cast<int64_t>(SH_CTAS) * num_sms();
   const int seg = a.dtype == GH_BF16 ? ShSeg<__nv_bfloat16>::COLS : ShSeg<float>::COLS;
@@ -1053,7 +1054,7 @@ void plan(ShapeArgs& a) {
     }
     if (tiles > 64 && a.R * tiles > 8 * slots) break;  // more ranges only add rounds
   }
-  const int64_t rows = static_cast<int64_t>(a.R) * a.ntiles / (4 * slots);
+  const int64_t rows = static_cast<int64_t>(a.R) * a.ntiles / (8 * slots);
   a.rows_per_cta = static_cast<int>(rows < 1 ? 1 : (rows > SH_MAX_ROWS ? SH_MAX_ROWS : rows));
   a.nseg = static_cast<int>(ceil_div(a.V, seg));
   const size_t in_elt = a.dtype == GH_BF16 ? 2 : 4, out_elt = a.out_dtype == GH_BF16 ? 2 : 4;

@@ -141,6 +141,34 @@ def test_rows_do_not_depend_on_the_batch(gpu_lib):
         assert torch.equal(g.grpo_adapter_logits(**part, out_dtype=torch.float32)["logits"], whole[rows])
 
 
+@pytest.mark.parametrize("n,V,rank", [(5, 50000, 8), (64, 60000, 16), (300, 45000, 32), (1500, 9000, 16)])
+def test_calls_queued_one_behind_the_other(gpu_lib, n, V, rank):
+    # many tiles per CTA, and calls on different rows and adapters that nothing waits between: each call's u and list
+    # take the workspace over from the call before
+    import gspo_logprob_gb300 as g
+    p = _problem(n, 64, V, 6, rank, "bf16", n)
+    d = _device(p, "bf16")
+    rng = np.random.default_rng(n)
+    sets = []
+    for k in range(5):
+        q = dict(p, H=_draw(rng, (n, 64), 1.0, "bf16"),
+                 adapter_id=np.sort(rng.integers(-1, 6, n)).astype(np.int32) if k % 2 else
+                 rng.integers(-1, 6, n).astype(np.int32))
+        sets.append((q, dict(d, H=torch.from_numpy(q["H"]).cuda().bfloat16(),
+                             adapter_id=torch.from_numpy(q["adapter_id"]).cuda())))
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    out = [g.grpo_adapter_logits(**s, status=st)["logits"] for _, s in sets + sets]
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    for k in range(5):
+        assert torch.equal(out[k], out[k + 5])
+        alone = g.grpo_adapter_logits(**sets[k][1])["logits"]
+        torch.cuda.synchronize()
+        assert torch.equal(out[k], alone)
+    _check(out[0], sets[0][0], "bf16", "bf16")
+
+
 def test_graph_stream_and_refusals(gpu_lib):
     import gspo_logprob_gb300 as g
     p = _problem(30, 128, 400, 4, 16, "bf16", 9)
