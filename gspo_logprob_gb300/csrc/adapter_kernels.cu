@@ -10,10 +10,9 @@
 // pass over the B_a in use and nothing is added to the logits afterwards.  Decode
 // batches are bound by the read of W (a row tile of requests multiplies every W
 // tile once), prompts by the tensor cores; a chunk is two MMAs of K = 16.
-// u is given as two bf16 terms, high and low, each its own MMA on the same B
-// chunk: one term alone would round u to 8 bits (an error of 2^-9 of the
-// adapter's part, visible in fp32 logits), both leave 2^-17, at 4 KB more
-// shared-memory traffic per chunk.
+// u is given as bf16 terms that add up to it, each its own MMA on the same B
+// chunk: two for bf16 logits (one alone would round u by 2^-9; two leave 2^-17),
+// three for fp32 logits, where the 2^-17 was two thirds of the error.
 //
 // fp32: exact fp32 FMA, no TF32, as the rest of the head.
 #include <cuda_bf16.h>
@@ -47,16 +46,29 @@ __device__ __forceinline__ float2 ad_dot8(const uint4& x, const uint4& y, float2
 }
 __device__ __forceinline__ uint4 ad_load8(const __nv_bfloat16* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 
+// Eight values rounded to bf16, which are taken off them: the next term.
+__device__ __forceinline__ uint4 ad_term(float* x) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+    x[2 * e] -= __low2float(p);
+    x[2 * e + 1] -= __high2float(p);
+    w[e] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // One CTA: RPC consecutive rows (of one row tile) times 8 RPW ranks, RPW of them
 // per warp.  It finds the adapters of the row tile in the order of their first
 // rows (the tile's slots), and writes its rows' part of every slot's chunks: u in
-// their own slot, 0 in the others.  U: [tiles, max_chunks, high/low, tile rows,
-// 16] bf16; list: per tile the number of slots, then each slot's adapter.
-// <1, 1> up to 1023 rows (one dot per warp), <8, 4> for prompts: the rows of a
+// their own slot, 0 in the others.  U: [tiles, max_chunks, terms, tile rows, 16]
+// bf16; list: per tile the number of slots, then each slot's adapter.
+// <1, 1> up to 1023 rows (one dot per warp), <8, 2> for prompts: the rows of a
 // request share a read of A_a, the ranks of a warp one of the rows (2048 rows,
-// rank 32, D = 4096: MEASURED_LOW us, against 170 with a dot at a time).
+// rank 32, D = 4096: 55 us, against 170 with a dot at a time).
 template <int RPC, int RPW>
-__global__ void __launch_bounds__(AD_THREADS) adapter_low_kernel(const AdapterArgs a) {
+__global__ void __launch_bounds__(AD_THREADS, 2) adapter_low_kernel(const AdapterArgs a) {
   constexpr int RANKS = AD_THREADS / 32 * RPW;
   __shared__ int ids[256];
   __shared__ int first[256];  // first row of the tile with the same adapter
@@ -94,7 +106,7 @@ __global__ void __launch_bounds__(AD_THREADS) adapter_low_kernel(const AdapterAr
   for (int q = 1; q < RPC; ++q) one &= ids[row0 - base + q] == id0;
   if (one) {
     const __nv_bfloat16* A1 = A0 + id0 * astep;
-#pragma unroll(RPC == 1 ? 4 : 1)
+#pragma unroll(RPC == 1 ? 4 : 2)
     for (int k = lane * 8; k < a.D; k += 256) {
       uint4 w[RPW], h[RPC];
 #pragma unroll
@@ -169,27 +181,20 @@ __global__ void __launch_bounds__(AD_THREADS) adapter_low_kernel(const AdapterAr
   // this CTA's ranks, eight (half a chunk) at a time, in every slot
   const int rc = a.rank_chunks;
   uint4* U = static_cast<uint4*>(a.U);
-  for (int i = tid; i < slots * RPC * RPW * 2; i += AD_THREADS) {
-    const int hl = i & 1, g = (i >> 1) % RPW, q = (i >> 1) / RPW % RPC, s = (i >> 1) / (RPW * RPC);
+  for (int i = tid; i < slots * RPC * RPW; i += AD_THREADS) {
+    const int g = i % RPW, q = i / RPW % RPC, s = i / (RPW * RPC);
     const int eight = blockIdx.y * RPW + g, chunk = eight >> 1, half = eight & 1;
     const int row = row0 + q - base;
     if (base + row >= a.N || chunk >= rc) continue;
-    uint32_t w[4] = {0, 0, 0, 0};
-    if (ids[row] >= 0 && slot_of[first[row]] == s) {
+    const bool own = ids[row] >= 0 && slot_of[first[row]] == s;
+    float x[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float x = u[q][8 * g + 2 * e], y = u[q][8 * g + 2 * e + 1];
-        if (hl) {  // what the rounding to the high term left
-          x -= __bfloat162float(__float2bfloat16_rn(x));
-          y -= __bfloat162float(__float2bfloat16_rn(y));
-        }
-        const __nv_bfloat162 p = __floats2bfloat162_rn(x, y);
-        w[e] = *reinterpret_cast<const uint32_t*>(&p);
-      }
+    for (int e = 0; e < 8; ++e) x[e] = own ? u[q][8 * g + e] : 0.f;
+    for (int t = 0; t < a.terms; ++t) {
+      const size_t at =
+          ((static_cast<size_t>(tile) * a.max_chunks + (s * rc + chunk)) * a.terms + t) * a.tile_rows + row;
+      U[at * 2 + half] = ad_term(x);
     }
-    const size_t at =
-        ((static_cast<size_t>(tile) * a.max_chunks + (s * rc + chunk)) * 2 + hl) * a.tile_rows + row;
-    U[at * 2 + half] = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -229,8 +234,11 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m
 // accumulator, about half an ulp per K = 16 step towards zero (1.3e-6 of the
 // logits at D = 1000, growing with D), so K is cut into segments of SEG_KB
 // blocks, each its own accumulator, which the epilogue adds up in registers with
-// rounding to nearest (3e-7).  A thread then holds a row of the tile: 128 columns
-// per tile, not 256.  bf16 logits round by 2^-9 anyway and keep one accumulator.
+// rounding to nearest (4.7e-7, whatever D; segments of 4 blocks leave 2.4e-7 and
+// cost 5 to 28%).  A thread then holds a row of the tile: 128 columns per tile,
+// not 256 (eight warps with 128 columns each of a 256-column tile spill: 819 us
+// against 755 for 2048 x 4096 x 32000).  bf16 logits round by 2^-9 anyway and
+// keep one accumulator.
 template <bool PAIR, bool EXACT>
 struct AdCfg {
   static constexpr int BN = EXACT ? 128 : TC_BN;  // widest tile
@@ -240,9 +248,11 @@ struct AdCfg {
   static constexpr int B_ROWS = PAIR ? BN / 2 : BN;
   static constexpr int STAGE_BYTES = A_BYTES + B_ROWS * TC_BK * 2;
   static constexpr int STAGES = 192 * 1024 / STAGE_BYTES;  // 192 KB in flight per SM
+  static constexpr int TERMS = EXACT ? 3 : 2;
   static constexpr int U_BYTES = TC_BM * 32;  // one term of a chunk
-  static constexpr int CHUNK_BYTES = 2 * U_BYTES + B_ROWS * 32;
-  static constexpr int CHUNKS = 2;  // low-rank chunks per stage
+  static constexpr int CHUNK_BYTES = TERMS * U_BYTES + B_ROWS * 32;
+  static constexpr int CHUNKS = EXACT ? 1 : 2;  // low-rank chunks per stage
+  static constexpr int LOW_WARPS = 4;  // epilogue warps that form u in the single-CTA form: a thread per row
   static constexpr int EPI_WARPS = 4;
   static constexpr int THREADS = 64 + 32 * EPI_WARPS;
   static constexpr int TURN_LD = 33;  // fp32 transpose tile of an epilogue warp
@@ -290,29 +300,21 @@ __device__ __forceinline__ void ad_item(const AdapterArgs& a, int row, int eight
     }
   }
   const float scale = on ? __ldg(a.scale + id) : 0.f;
-  uint32_t hi[4], lo[4];
+  float x[8];
 #pragma unroll
-  for (int t = 0; t < 8; t += 2) {
-    float v[2];
+  for (int t = 0; t < 8; ++t) {
+    float v = acc[t].x + acc[t].y;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      v[e] = acc[t + e].x + acc[t + e].y;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v[e] += __shfl_xor_sync(0xffffffffu, v[e], o);
-      v[e] = on ? v[e] * scale : 0.f;
-    }
-    __nv_bfloat162 p = __floats2bfloat162_rn(v[0], v[1]);
-    hi[t / 2] = *reinterpret_cast<const uint32_t*>(&p);
-    p = __floats2bfloat162_rn(v[0] - __low2float(p), v[1] - __high2float(p));
-    lo[t / 2] = *reinterpret_cast<const uint32_t*>(&p);
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    x[t] = on ? v * scale : 0.f;
   }
   uint4* U = static_cast<uint4*>(a.U);
-  for (int s = lane; s < 2 * slots; s += 32) {
-    const int hl = s & 1, at_slot = s >> 1;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (id >= 0 && at_slot == slot) w = hl ? make_uint4(lo[0], lo[1], lo[2], lo[3]) : make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    const size_t r = (static_cast<size_t>(at_slot * a.rank_chunks + (eight >> 1)) * 2 + hl) * a.tile_rows + row;
-    U[r * 2 + (eight & 1)] = w;
+  for (int t = 0; t < a.terms; ++t) {
+    const uint4 w = ad_term(x);
+    for (int s = lane; s < slots; s += 32) {
+      const size_t r = (static_cast<size_t>(s * a.rank_chunks + (eight >> 1)) * a.terms + t) * a.tile_rows + row;
+      U[r * 2 + (eight & 1)] = id >= 0 && s == slot ? w : make_uint4(0, 0, 0, 0);
+    }
   }
 }
 
@@ -388,7 +390,7 @@ __global__ void __launch_bounds__(AdCfg<PAIR, EXACT>::THREADS, 1)
   __shared__ int first_s[PAIR ? 1 : TC_BM];  // the first row with it
   __shared__ int slot_s[PAIR ? 1 : TC_BM];   // that row's slot
   __shared__ int list_s[PAIR ? 1 : TC_BM + 1];
-  __shared__ int count_s[C::EPI_WARPS];
+  __shared__ int count_s[C::LOW_WARPS];
   uint64_t* listed = drain + 1;  // single-CTA form: the slots are in list_s
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0;  // the even CTA of a pair issues its MMAs
@@ -403,7 +405,7 @@ __global__ void __launch_bounds__(AdCfg<PAIR, EXACT>::THREADS, 1)
       mbar_init(&tempty[b], (PAIR ? 2 : 1) * C::EPI_WARPS);
     }
     mbar_init(drain, 1);
-    mbar_init(listed, C::EPI_WARPS);
+    mbar_init(listed, C::LOW_WARPS);
     *abort_flag = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
@@ -487,21 +489,21 @@ __global__ void __launch_bounds__(AdCfg<PAIR, EXACT>::THREADS, 1)
         if (!PAIR && ok && !ready) {
           // u is complete when every epilogue warp of the grid has counted itself
           ok = mbar_wait_bounded(listed, 0, abort_flag, a.status, GH_DEV_TIMEOUT, timeout_ns) &&
-               count_wait_bounded(a.counter, C::EPI_WARPS * gridDim.x, abort_flag, a.status, timeout_ns);
+               count_wait_bounded(a.counter, C::LOW_WARPS * gridDim.x, abort_flag, a.status, timeout_ns);
           asm volatile("fence.proxy.async;" ::: "memory");  // u is read by the asynchronous proxy
           ready = true;
         }
         const int chunks = ok ? min(max(list[0] * rc, 0), a.max_chunks) : 0;
         for (int c0 = 0; ok && c0 < chunks; c0 += C::CHUNKS) {
           const int n = min(C::CHUNKS, chunks - c0);
-          if (!open_stage(n * (2 * a_rows + b_rows) * 32)) break;
+          if (!open_stage(n * (C::TERMS * a_rows + b_rows) * 32)) break;
           for (int q = 0; q < n; ++q) {
             uint8_t* s = smem + stage * C::STAGE_BYTES + q * C::CHUNK_BYTES;
             const int c = c0 + q;
-            const int u0 = ((m_blk * a.max_chunks + c) * 2) * a.tile_rows + static_cast<int>(rank) * TC_BM;
-            load3(s, &tmU, 0, u0, 0);
-            load3(s + C::U_BYTES, &tmU, 0, u0 + a.tile_rows, 0);
-            load3(s + 2 * C::U_BYTES, &tmB, (c % rc) * 16, n0, list[1 + c / rc]);
+            const int u0 = (m_blk * a.max_chunks + c) * C::TERMS * a.tile_rows + static_cast<int>(rank) * TC_BM;
+#pragma unroll
+            for (int t = 0; t < C::TERMS; ++t) load3(s + t * C::U_BYTES, &tmU, 0, u0 + t * a.tile_rows, 0);
+            load3(s + C::TERMS * C::U_BYTES, &tmB, (c % rc) * 16, n0, list[1 + c / rc]);
           }
           close_stage();
         }
@@ -604,9 +606,9 @@ __global__ void __launch_bounds__(AdCfg<PAIR, EXACT>::THREADS, 1)
           const int n = min(C::CHUNKS, chunks - c0);
           for (int q = 0; q < n; ++q) {
             const uint32_t ub = smem_u32(smem + stage * C::STAGE_BYTES + q * C::CHUNK_BYTES);
-            const uint64_t bd = sdesc_sw32(ub + 2 * C::U_BYTES);
-            mma(d, sdesc_sw32(ub), bd, 1u);
-            mma(d, sdesc_sw32(ub + C::U_BYTES), bd, 1u);
+            const uint64_t bd = sdesc_sw32(ub + C::TERMS * C::U_BYTES);
+#pragma unroll
+            for (int t = 0; t < C::TERMS; ++t) mma(d, sdesc_sw32(ub + t * C::U_BYTES), bd, 1u);
           }
           free_stage();
         }
@@ -628,8 +630,8 @@ __global__ void __launch_bounds__(AdCfg<PAIR, EXACT>::THREADS, 1)
     const int sub = warp & 3;  // TMEM lane quarter this warp may access
     const uint32_t lane_addr = static_cast<uint32_t>(sub * 32) << 16;
     float* turn = turn_all + (warp - 2) * (C::TURN_BYTES / 4);
-    if constexpr (!PAIR) {
-      static_assert(C::EPI_WARPS * 32 == TC_BM, "a thread per row");
+    if (!PAIR && warp - 2 < C::LOW_WARPS) {
+      static_assert(C::LOW_WARPS * 32 == TC_BM, "a thread per row");
       const int et = threadIdx.x - 64, ew = warp - 2;
       const auto sync_epilogue = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
       int id = et < a.N ? a.ids[et] : -1;
@@ -653,7 +655,7 @@ __global__ void __launch_bounds__(AdCfg<PAIR, EXACT>::THREADS, 1)
       if (lane == 0) count_s[ew] = __popc(leads);
       sync_epilogue();
       int off = __popc(leads & ((1u << lane) - 1u)), slots = 0;
-      for (int w = 0; w < C::EPI_WARPS; ++w) {
+      for (int w = 0; w < C::LOW_WARPS; ++w) {
         if (w < ew) off += count_s[w];
         slots += count_s[w];
       }
@@ -663,7 +665,7 @@ __global__ void __launch_bounds__(AdCfg<PAIR, EXACT>::THREADS, 1)
       sync_epilogue();
       if (lane == 0) mbar_arrive(listed);
       const int eights = 2 * rc;
-      for (int item = blockIdx.x * C::EPI_WARPS + ew; item < a.N * eights; item += gridDim.x * C::EPI_WARPS)
+      for (int item = blockIdx.x * C::LOW_WARPS + ew; item < a.N * eights; item += gridDim.x * C::LOW_WARPS)
         ad_item(a, item / eights, item % eights, ids_s[item / eights], slot_s[first_s[item / eights]], slots, lane);
       asm volatile("fence.proxy.async;" ::: "memory");
       __threadfence();
@@ -906,7 +908,7 @@ cudaError_t launch_product(const AdapterArgs& a, cudaStream_t st) {
   CUtensorMap th, tw, tu, tb;
   const uint64_t row_bytes = static_cast<uint64_t>(a.D) * 2;
   const int tiles = static_cast<int>(ceil_div(a.N, a.tile_rows));
-  const uint64_t u_rows = static_cast<uint64_t>(tiles) * a.max_chunks * 2 * a.tile_rows;
+  const uint64_t u_rows = static_cast<uint64_t>(tiles) * a.max_chunks * C::TERMS * a.tile_rows;
   if (!make_tmap_bf16(&th, a.H, a.D, a.N, row_bytes, TC_BK, a_rows) ||
       !make_tmap_bf16(&tw, a.W, a.D, a.V, row_bytes, TC_BK, b_rows) ||
       !make_tmap_bf16_k16(&tu, a.U, 16, u_rows, 1, 32, u_rows * 32, a_rows) ||
@@ -937,7 +939,7 @@ cudaError_t launch_product(const AdapterArgs& a, cudaStream_t st) {
     attr[0].val.clusterDim.z = 1;
   } else {
     // CTAs without a tile help with u
-    const int64_t share = ceil_div(static_cast<int64_t>(a.N) * 2 * a.rank_chunks, C::EPI_WARPS);
+    const int64_t share = ceil_div(static_cast<int64_t>(a.N) * 2 * a.rank_chunks, C::LOW_WARPS);
     const int helped = static_cast<int>(share < most ? share : most);
     if (static_cast<int>(cfg.gridDim.x) < helped) cfg.gridDim.x = helped;
     attr[0].id = cudaLaunchAttributeCooperative;
@@ -955,15 +957,16 @@ cudaError_t launch_product(const AdapterArgs& a, cudaStream_t st) {
 }  // namespace
 
 // Rows up to one single-CTA tile (128) take that form; more take pairs.
-AdapterPlan adapter_plan(int64_t N, int64_t rank, int64_t num_adapters) {
+AdapterPlan adapter_plan(int64_t N, int64_t rank, int64_t num_adapters, int out_dtype) {
   AdapterPlan p;
+  p.terms = out_dtype == GH_FP32 ? AdCfg<false, true>::TERMS : AdCfg<false, false>::TERMS;
   p.tile_rows = N <= TC_BM ? TC_BM : 2 * TC_BM;
   p.rank_chunks = static_cast<int>(ceil_div(rank, 16));
   const int64_t slots = num_adapters < p.tile_rows ? num_adapters : p.tile_rows;
   p.max_chunks = static_cast<int>(slots * p.rank_chunks);
   p.list_ld = 1 + static_cast<int>(slots);
   const int64_t tiles = ceil_div(N, p.tile_rows);
-  p.u_rows = tiles * p.max_chunks * 2 * p.tile_rows;
+  p.u_rows = tiles * p.max_chunks * p.terms * p.tile_rows;
   p.u_bytes = align_up(static_cast<size_t>(p.u_rows) * 32, 256);
   p.list_bytes = align_up(static_cast<size_t>(tiles) * p.list_ld * 4, 256);  // or the counter, with one row tile
   return p;
@@ -980,7 +983,7 @@ cudaError_t launch_adapter_low(const AdapterArgs& a, cudaStream_t st) {
     if (a.N < 1024)
       adapter_low_kernel<1, 1><<<dim3(a.N, eights), AD_THREADS, 0, st>>>(a);
     else
-      adapter_low_kernel<8, 4><<<dim3(static_cast<unsigned>(ceil_div(a.N, 8)), static_cast<unsigned>(ceil_div(eights, 4))),
+      adapter_low_kernel<8, 2><<<dim3(static_cast<unsigned>(ceil_div(a.N, 8)), static_cast<unsigned>(ceil_div(eights, 2))),
                                  AD_THREADS, 0, st>>>(a);
   }
   return cudaGetLastError();

@@ -947,7 +947,7 @@ static gh_status check_adapter(const gh_adapter* p) {
     if (p->D % 8 != 0 || p->rank % 8 != 0)
       return fail(GH_ERR_INVALID_ARG, "bf16 needs D %% 8 == 0 and rank %% 8 == 0 (D=%lld, rank=%d)", (long long)p->D,
                   p->rank);
-    if (adapter_plan(p->N, p->rank, p->num_adapters).u_rows > INT32_MAX)
+    if (adapter_plan(p->N, p->rank, p->num_adapters, p->out_dtype).u_rows > INT32_MAX)
       return fail(GH_ERR_INVALID_ARG, "N x adapters x rank is too large for one call: split the rows");
   } else if (ceil_div(p->N, 64) > 65535 || p->N * p->rank > INT32_MAX) {
     return fail(GH_ERR_INVALID_ARG, "N=%lld is too large for one fp32 call: split the rows", (long long)p->N);
@@ -960,7 +960,7 @@ static gh_status check_adapter(const gh_adapter* p) {
 size_t grpo_adapter_logits_workspace_size(const gh_adapter* p) {
   if (check_adapter(p) != GH_OK) return 0;
   if (p->dtype == GH_FP32) return align_up(static_cast<size_t>(p->N) * p->rank * 4, 256);
-  const AdapterPlan q = adapter_plan(p->N, p->rank, p->num_adapters);
+  const AdapterPlan q = adapter_plan(p->N, p->rank, p->num_adapters, p->out_dtype);
   return q.u_bytes + q.list_bytes;
 }
 
@@ -988,7 +988,7 @@ gh_status grpo_adapter_logits(const gh_adapter* p, int32_t* status, void* ws, si
   if (!device_is_sm103()) return fail(GH_ERR_UNSUPPORTED, "current device is not an sm_103 (GB300) GPU");
   if (p->N == 0) return GH_OK;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const AdapterPlan q = adapter_plan(p->N, p->rank, p->num_adapters);
+  const AdapterPlan q = adapter_plan(p->N, p->rank, p->num_adapters, p->out_dtype);
   AdapterArgs a{};
   a.N = static_cast<int>(p->N);
   a.D = static_cast<int>(p->D);
@@ -1013,6 +1013,7 @@ gh_status grpo_adapter_logits(const gh_adapter* p, int32_t* status, void* ws, si
   a.rank_chunks = q.rank_chunks;
   a.max_chunks = q.max_chunks;
   a.list_ld = q.list_ld;
+  a.terms = q.terms;
   a.status = status;
   cudaError_t e = cudaSuccess;
   if (adapter_low_apart(a)) {

@@ -295,10 +295,11 @@ struct AdapterPlan {
   int rank_chunks;  // 16-wide chunks of a rank
   int max_chunks;   // chunks a row tile may have
   int list_ld;
+  int terms;        // bf16 terms that add up to u
   int64_t u_rows;   // rows of 16 elements
   size_t u_bytes, list_bytes;
 };
-AdapterPlan adapter_plan(int64_t N, int64_t rank, int64_t num_adapters);
+AdapterPlan adapter_plan(int64_t N, int64_t rank, int64_t num_adapters, int out_dtype);
 struct AdapterArgs {
   int N, D, V, rank, num_adapters;
   int dtype, out_dtype;
@@ -314,7 +315,7 @@ struct AdapterArgs {
   void* U;       // bf16 [u_rows, 16], or fp32 [N, rank]
   int32_t* list;
   int* counter;  // bf16, one row tile: the warps of the launch that have written their part of U
-  int tile_rows, rank_chunks, max_chunks, list_ld;
+  int tile_rows, rank_chunks, max_chunks, list_ld, terms;
   int* status;
 };
 // u, unless the product computes it itself (bf16, one row tile)

@@ -12,10 +12,11 @@
 // One kernel serves the three calls.  A CTA owns a range of columns for a block
 // of rows.  What a row's history and bias list say about its tokens is kept in
 // shared memory as a ranked set: a bit per column that is in the set, the set's
-// size before each 32 columns, and one word per member (output count, prompt
-// flag, bias entry) at its rank.  That is 6 bytes per 32 columns and 4 per
-// distinct token, against 4 bytes per column for a table of words, so a CTA can
-// take a fifth of a 151936-column row and a history is scanned 5 times, not 10.
+// size before each 32 columns, and at each member's rank its column and one word
+// (output count, prompt flag, bias entry).  That is 6 bytes per 32 columns and 6
+// per distinct token, against 4 bytes per column for a table of words, so a CTA
+// takes a quarter of a 151936-column row and a history is scanned 4 times, not
+// 10.  With more than SH_SET members the range is taken in parts.
 //
 // Rows whose history is that of the row before plus some tokens (consecutive
 // rows of a training sequence) form a chain: the set is built once, from the
@@ -26,16 +27,30 @@
 // Columns are cut into segments of 4 (bf16; fp32: 2) chunks of 256 columns, 2 KB
 // of a row.  A warp stages its segments in shared memory by asynchronous copies,
 // one ahead of the one it works on (64 KB in flight per SM, which covers the
-// latency of HBM at its rate); it reads the allow bits one segment earlier still,
-// so that barred logits are not copied.  Rows that do not start on a 16-byte
-// boundary are copied from the boundary before and shifted by words as they are
-// read back.  A segment has a sparse pass over the members, a lane per 32
-// columns, and a dense pass, lane l taking columns 8l..8l+7 of a chunk.  The
-// log-prob's sparse pass puts -inf in the members' staged places, so that the
-// dense pass knows nothing of them; shaped logits and gradients are overwritten
-// at the members after the dense pass.  The log-prob keeps one (max, sum) per row
-// and segment, so its bits depend on V and the type alone: not on the columns or
-// rows per CTA, the strides or the other rows of the batch.
+// latency of HBM at its rate; three CTAs with two ahead were 5% slower); it reads
+// the allow bits one segment earlier still, so that barred logits are not copied.
+// Rows that do not start on a 16-byte boundary are copied from the boundary
+// before and shifted by words as they are read back.
+//
+// A segment has a sparse pass over its members, whose ranks are consecutive, a
+// lane each; and a dense pass over the stage, lane l taking columns 8l..8l+7 of a
+// chunk, in packed pairs of fp32.  The log-prob's sparse pass puts -inf in the
+// members' staged places, so that the dense pass knows nothing of them; shaped
+// logits and gradients are overwritten at the members after the dense pass.
+// Where a mask leaves few tokens they are visited one by one instead.
+//
+// The log-prob keeps one (max, sum) per row and segment.  Its dense part adds in
+// an order that depends on V and the type alone, its members' part adds integers,
+// so the bits do not depend on the columns or rows per CTA, the chain, the
+// strides or the other rows of the batch.
+//
+// Bounds and measurements (GB300, 6.79 TB/s copy): 8192 rows of 151936 bf16 logits
+// in packed sequences, 55-62% of the rows live: log-prob 244-289 us at 85-90% of
+// the copy rate (with a word per column and no staging: 958), gradient 542-569 us
+// at 96% (1338).  256 decode rows: 45 us shaped, 50 us log-prob, for 20 and 9 us of
+// traffic: two rounds of CTAs whose set-up, set and first copies (about 10 us a
+// round) are latency, not traffic.  At 415 instructions a segment the issue slots
+// are 60% full; without allow masks a leaner instance runs.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -55,8 +70,8 @@ constexpr int SH_KEEP = 8;                       // history tokens a thread keep
 constexpr int SH_MAX_ROWS = 32;                  // rows per CTA (one lane each in the set-up)
 constexpr float SH_LOG2E = 1.4426950408889634f;
 constexpr float SH_LOWEST = 3.402823466e38f;     // the largest finite fp32
-constexpr float SH_ONE = 1099511627776.f;          // 2^40: 1 in the sum over the members
-constexpr int SH_FEW = 4;
+constexpr float SH_ONE = 1099511627776.f;        // 2^40: 1 in the sum over the members
+constexpr int SH_FEW = 4;                        // a mask with at most this many of any 32 columns is walked, not swept
 constexpr float SH_BIG = 1e37f;                  // beyond this a step to base 2 may overflow
 static_assert(SH_SET % SHAPE_MIN_SEG == 0, "a range of SH_SET columns, which always fits, is whole segments");
 
@@ -440,7 +455,7 @@ constexpr int SH_TILE = 2048 + 16;  // a segment and the 16 bytes that an unalig
 // output is written element by element where its rows are not aligned.
 // MASKS: rows may carry an allow mask.
 template <class TIn, class TOut, int MODE, bool ALIGNED, bool OUT_TILE, bool MASKS>
-__global__ void __launch_bounds__(SH_THREADS, OUT_TILE ? 2 : SH_CTAS) shape_kernel(const ShapeArgs a) {
+__global__ void __launch_bounds__(SH_THREADS, OUT_TILE ? 3 : SH_CTAS) shape_kernel(const ShapeArgs a) {
   using S = ShSeg<TIn>;
   constexpr int CB = 256 * sizeof(TIn);  // bytes of a chunk
   extern __shared__ __align__(16) uint8_t sh_smem[];

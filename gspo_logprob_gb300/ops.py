@@ -716,8 +716,10 @@ def grpo_shape_logits(logits, shaping: Shaping, *, out=None, out_dtype=None, sta
     (default: the logits' type).  Returns a dict with logits and status."""
     dt, ld = _need_logits(logits, "logits", shaping)
     if out is None:
-        out = torch.empty(logits.shape, dtype=out_dtype or logits.dtype, device=logits.device)
-    odt, old = _need_logits(out, "out", shaping, out_dtype)
+        out = torch.empty(shaping.shape, dtype=out_dtype or logits.dtype, device=logits.device)
+        odt, old = _gh_dtype(out.dtype, "out_dtype"), max(shaping.shape[1], 1)
+    else:
+        odt, old = _need_logits(out, "out", shaping, out_dtype)
     dev = logits.device
     st = new_status(dev) if status is None else status
     code = _lib().grpo_shape_logits(shaping.ref, logits.data_ptr(), dt, ld, out.data_ptr(), odt, old, st.data_ptr(),
@@ -770,8 +772,9 @@ def grpo_shaped_logp_backward(logits, targets, mask, shaping: Shaping, lse, coef
         _need(grad_out, "grad_out", _F32)
     dev = logits.device
     if dlogits is None:
-        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
-    _, dld = _need_logits(dlogits, "dlogits", shaping, logits.dtype)
+        dlogits, dld = torch.empty(shaping.shape, dtype=logits.dtype, device=dev), max(shaping.shape[1], 1)
+    else:
+        _, dld = _need_logits(dlogits, "dlogits", shaping, logits.dtype)
     st = new_status(dev) if status is None else status
     code = _lib().grpo_shaped_logp_backward(shaping.ref, logits.data_ptr(), dt, ld, targets.data_ptr(),
                                             mask.data_ptr(), lse.data_ptr(), coef.data_ptr(),

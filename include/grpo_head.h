@@ -406,8 +406,8 @@ typedef struct {
 /* Bytes of scratch `ws` grpo_adapter_logits needs (0 for invalid arguments). */
 size_t grpo_adapter_logits_workspace_size(const gh_adapter* problem);
 /*
- * A bf16 call sums each A_a h_i in fp32 and carries it as two bf16 terms, so
- * that the logits have the accuracy of fp32 accumulation whatever out_dtype.
+ * A bf16 call sums each A_a h_i in fp32 and carries it as two bf16 terms (three
+ * for fp32 logits), so that the logits have the accuracy of fp32 accumulation.
  * A row's logits do not depend on the other rows' values or adapters as long
  * as the weights are finite: the rows of a tile multiply the B_a of the
  * others by zero, so a NaN or infinity in a B_a in use reaches all of them.

@@ -55,6 +55,8 @@ def test_workspace_size(lib):
     # two 256-row tiles, rank 24 takes two chunks
     assert lib.grpo_adapter_logits_workspace_size(ctypes.byref(_p(N=300, rank=24))) == \
         al(2 * 8 * 2 * 256 * 32) + al(2 * 5 * 4)
+    # fp32 logits: three terms
+    assert lib.grpo_adapter_logits_workspace_size(ctypes.byref(_p(out_dtype=1))) == al(4 * 3 * 128 * 32) + al(5 * 4)
     assert lib.grpo_adapter_logits_workspace_size(ctypes.byref(_p(dtype=1, out_dtype=1, rank=3))) == al(64 * 3 * 4)
     assert lib.grpo_adapter_logits_workspace_size(ctypes.byref(_p(rank=0))) == 0
 

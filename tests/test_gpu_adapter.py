@@ -5,7 +5,7 @@ Tolerances, with eps = 2^-24 and M the sum of the absolute terms of a logit:
    within K eps M of exact in the worst case and sqrt(K) eps M typically: 4
    sqrt(D + rank) eps M is allowed (tensor cores may align a group of products
    before they add it: the factor 4);
- * u is carried in two bf16 terms: 2^-16 of the adapter's part, at most M;
+ * u is carried in two or three bf16 terms: 2^-16 of the adapter's part, at most M;
    fp32 calls have neither and the same sum bound;
  * a bf16 output: half an ulp, 2^-8 of the value."""
 import numpy as np
