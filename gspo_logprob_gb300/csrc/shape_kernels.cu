@@ -44,13 +44,15 @@
 // so the bits do not depend on the columns or rows per CTA, the chain, the
 // strides or the other rows of the batch.
 //
-// Bounds and measurements (GB300, 6.79 TB/s copy): 8192 rows of 151936 bf16 logits
-// in packed sequences, 55-62% of the rows live: log-prob 244-289 us at 85-90% of
-// the copy rate (with a word per column and no staging: 958), gradient 542-569 us
-// at 96% (1338).  256 decode rows: 45 us shaped, 50 us log-prob, for 20 and 9 us of
-// traffic: two rounds of CTAs whose set-up, set and first copies (about 10 us a
-// round) are latency, not traffic.  At 415 instructions a segment the issue slots
-// are 60% full; without allow masks a leaner instance runs.
+// Bounds and measurements (GB300, 6.79 TB/s copy; 4096 rows of 151936 bf16 logits
+// in packed sequences, 2451 of them live): log-prob 164 us for 745 MB (67% of the
+// copy rate; 128 us without histories; 75% of the issue slots full, 410
+// instructions a segment of which the dense pass takes 300 and the members 100),
+// gradient 295 us for 1.93 GB (96%).  The first form, a word per column and no
+// staging, took 480 and 670.  256 decode rows: 45 us shaped, 50 us log-prob, for 20
+// and 9 us of traffic: two rounds of CTAs whose set-up, set and first copies
+// (about 10 us a round) are latency, not traffic.  Without allow masks a leaner
+// instance runs.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -70,7 +72,7 @@ constexpr int SH_KEEP = 8;                       // history tokens a thread keep
 constexpr int SH_MAX_ROWS = 32;                  // rows per CTA (one lane each in the set-up)
 constexpr float SH_LOG2E = 1.4426950408889634f;
 constexpr float SH_LOWEST = 3.402823466e38f;     // the largest finite fp32
-constexpr float SH_ONE = 1099511627776.f;        // 2^40: 1 in the sum over the members
+constexpr float SH_ONE = 67108864.f;             // 2^26: 1 in the sum over the members
 constexpr int SH_FEW = 4;                        // a mask with at most this many of any 32 columns is walked, not swept
 constexpr float SH_BIG = 1e37f;                  // beyond this a step to base 2 may overflow
 static_assert(SH_SET % SHAPE_MIN_SEG == 0, "a range of SH_SET columns, which always fits, is whole segments");
@@ -441,8 +443,7 @@ __device__ __forceinline__ float sh_member(const ShPen& p, uint32_t w, float x, 
   slope = (w & (SH_COUNT | SH_PROMPT)) ? (x > 0.f ? p.inv_rep : p.rep) : 1.f;
   x = x * slope - (c ? fmaf(p.freq, static_cast<float>(c), p.pres) : 0.f);
   const uint32_t b = w >> SH_BIAS_SHIFT;
-  if (b) x += __ldg(p.bias + b);
-  return x;
+  return b ? x + __ldg(p.bias + b) : x;
 }
 
 // Shared memory of a CTA: the set, then each warp's stages and (unaligned
@@ -720,45 +721,54 @@ __global__ void __launch_bounds__(SH_THREADS, OUT_TILE ? 3 : SH_CTAS) shape_kern
         const bool few = masked && __reduce_max_sync(0xffffffffu, __popc(okw)) <= SH_FEW;
 
         if (MODE == SHAPE_LOGP) {
-          // members: their values go into a sum of integers (units of 2^-40 of the largest), which does not depend on
-          // the order, as ranks depend on the rows of the chain; their staged places get -inf
-          float zm = -INFINITY, z0 = -INFINITY;
-          unsigned long long fixed = 0;
-          bool mine_is_target = false, nan = false;
-          if (r1 > r0) {
-            const auto value = [&](int q, int& j) {
-              const uint32_t w = set.word[q];
-              j = -1;
-              if (!w) return -INFINITY;
-              j = set.col[q];
-              float slope;
-              return allowed(j) ? sh_member(pen, w, sh_to_float<TIn>(x[j - seg]), slope) * inv_t : -INFINITY;
-            };
-            int j0 = -1, j;
-            if (r0 + lane < r1) z0 = value(r0 + lane, j0);
-            zm = z0;
-            for (int q = r0 + 32 + lane; q < r1; q += 32) zm = fmaxf(zm, value(q, j));
-            zm = fmaxf(sh_warp_max(zm), -SH_LOWEST);  // the lowest finite value in place of -inf
-            const auto add = [&](float z, int at) {
-              if (at < 0) return;
-              const float e = ex2_approx((z - zm) * SH_LOG2E);
-              nan |= e != e;
-              fixed += static_cast<unsigned long long>(e * SH_ONE);
-              if (at == y) {
-                a.zy[row] = z;
-                mine_is_target = true;
+          if (sg == ysg) {
+            // the target, before the members' places change
+            if (lane == 0) {
+              float z = -INFINITY;
+              if (allowed(y)) {
+                const bool member = ranked && ((set.member[static_cast<uint32_t>(y) >> 5] >> (y & 31)) & 1u) != 0;
+                float slope;
+                z = sh_member(pen, member ? set.word[set.rank(static_cast<uint32_t>(y))] : 0u, sh_to_float<TIn>(x[y - seg]), slope) * inv_t;
               }
-              x[at - seg] = sh_from_float<TIn>(-INFINITY);
-            };
-            add(z0, j0);
-            for (int q = r0 + 32 + lane; q < r1; q += 32) {
-              const float z = value(q, j);
-              add(z, j);
+              a.zy[row] = z;
             }
-            mine_is_target = __any_sync(0xffffffffu, mine_is_target);
             __syncwarp();
           }
-          if (sg == ysg && !mine_is_target && lane == 0) a.zy[row] = allowed(y) ? sh_to_float<TIn>(x[y - seg]) * inv_t : -INFINITY;
+          // members: their exponentials go into a sum of integers (units of 2^-26 of the largest), which does not depend
+          // on the order, as ranks depend on the rows of the chain; their staged places get -inf
+          float zm = -INFINITY;
+          uint32_t fixed = 0;
+          bool nan = false;
+          if (r1 > r0) {
+            // rank q's shaped value and column (lanes past the last rank: -inf and -1); no branches
+            const auto value = [&](int q, int& at) {
+              const uint32_t w = q < r1 ? set.word[q] : 0u;
+              const int j = set.col[min(q, r1 - 1)];
+              float slope;
+              const float z = sh_member(pen, w, sh_to_float<TIn>(x[j - seg]), slope) * inv_t;
+              at = w ? j : -1;
+              return w && allowed(j) ? z : -INFINITY;
+            };
+            const auto add = [&](float z, int j) {
+              const float e = ex2_approx((z - zm) * SH_LOG2E);
+              nan |= e != e;
+              fixed += __float2uint_rn(e * SH_ONE);
+              if (j >= 0) x[j - seg] = sh_from_float<TIn>(-INFINITY);
+            };
+            int j0 = -1, j;
+            const float z0 = value(r0 + lane, j0);
+            zm = z0;
+            if (r1 - r0 > 32)
+              for (int q = r0 + 32 + lane; q < r1; q += 32) zm = fmaxf(zm, value(q, j));
+            zm = fmaxf(sh_warp_max(zm), -SH_LOWEST);  // the lowest finite value in place of -inf
+            add(z0, j0);
+            if (r1 - r0 > 32)
+              for (int q = r0 + 32 + lane; q < r1; q += 32) {
+                const float z = value(q, j);
+                add(z, j);
+              }
+            __syncwarp();
+          }
           float m = -INFINITY, sum = 0.f, ml = -INFINITY, sl = 0.f;
           ShRaw<TIn> raw[S::CHUNKS];
           if (few) {
@@ -838,15 +848,18 @@ __global__ void __launch_bounds__(SH_THREADS, OUT_TILE ? 3 : SH_CTAS) shape_kern
               }
             }
           }
+          if (nan) sum = __int_as_float(0x7fc00000);
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
           if (r1 > r0) {
-            // at most 1024 members: the high parts add up to below 2^31, the low ones to 2^30
-            const uint32_t hi = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(fixed >> 20));
-            const uint32_t lo = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(fixed) & 0xfffffu);
-            const float t = static_cast<float>((static_cast<unsigned long long>(hi) << 20) + lo) * (1.f / SH_ONE);
-            sum += t * ex2_approx((zm - ref) * SH_LOG2E);
-            if (__any_sync(0xffffffffu, nan)) sum = __int_as_float(0x7fc00000);
+            // a lane has at most 32 members: below 2^32; so have 32 lanes one each
+            float t;
+            if (r1 - r0 <= 32)
+              t = static_cast<float>(__reduce_add_sync(0xffffffffu, fixed));
+            else
+              t = fmaf(static_cast<float>(__reduce_add_sync(0xffffffffu, fixed >> 16)), 65536.f,
+                       static_cast<float>(__reduce_add_sync(0xffffffffu, fixed & 0xffffu)));
+            sum += t * (1.f / SH_ONE) * ex2_approx((zm - ref) * SH_LOG2E);
           }
           if (lane == 0) part[sg] = make_float2(m, sum);
         } else {
