@@ -280,7 +280,7 @@ struct ShapeArgs {
   float* lse_out;
   int* status;
   // set by the launchers
-  int cols, ntiles, rows_per_cta, nseg;
+  int cols, ntiles, rows_per_cta, nseg, room;
   bool vec_in, vec_out;
 };
 int64_t shape_segments(int64_t V);

@@ -16,7 +16,8 @@
 // (output count, prompt flag, bias entry).  That is 6 bytes per 32 columns and 6
 // per distinct token, against 4 bytes per column for a table of words, so a CTA
 // takes a quarter of a 151936-column row and a history is scanned 4 times, not
-// 10.  With more than SH_SET members the range is taken in parts.
+// 10.  With more members than the set has room for (2048, or 3072 of up to
+// 6144 columns) the range is taken in parts.
 //
 // Rows whose history is that of the row before plus some tokens (consecutive
 // rows of a training sequence) form a chain: the set is built once, from the
@@ -67,7 +68,7 @@ constexpr int SH_THREADS = 256;
 constexpr int SH_WARPS = SH_THREADS / 32;
 constexpr int SH_CTAS = 4;                       // resident per SM: 32 warps of 64 registers a thread
 constexpr int SH_MAX_COLS = 38912;               // columns per CTA
-constexpr int SH_SET = 2048;                     // members the words have room for
+constexpr int SH_SET_BYTES = 19712;               // of a set: SH_MAX_COLS columns with 2048 members, fewer with more
 constexpr int SH_KEEP = 8;                       // history tokens a thread keeps while it builds a set
 constexpr int SH_MAX_ROWS = 32;                  // rows per CTA (one lane each in the set-up)
 constexpr float SH_LOG2E = 1.4426950408889634f;
@@ -75,7 +76,6 @@ constexpr float SH_LOWEST = 3.402823466e38f;     // the largest finite fp32
 constexpr float SH_ONE = 67108864.f;             // 2^26: 1 in the sum over the members
 constexpr int SH_FEW = 4;                        // a mask with at most this many of any 32 columns is walked, not swept
 constexpr float SH_BIG = 1e37f;                  // beyond this a step to base 2 may overflow
-static_assert(SH_SET % SHAPE_MIN_SEG == 0, "a range of SH_SET columns, which always fits, is whole segments");
 
 template <class T>
 struct ShSeg {
@@ -328,8 +328,8 @@ __device__ __forceinline__ bool sh_load_row(const ShapeArgs& a, int row, ShRow& 
 // built; a member whose word is 0 belongs to later rows of the chain only.
 struct ShSet {
   uint32_t* member;  // [cols / 32] a bit per column
-  uint32_t* word;    // [SH_SET]
-  uint16_t* col;     // [SH_SET] a member's column, by rank
+  uint32_t* word;    // [room]
+  uint16_t* col;     // [room] a member's column, by rank
   uint16_t* before;  // [cols / 32 + 1] members before each 32 columns
   __device__ __forceinline__ uint32_t rank(uint32_t j) const {
     return before[j >> 5] + __popc(member[j >> 5] & ((1u << (j & 31)) - 1u));
@@ -348,7 +348,7 @@ __device__ __forceinline__ void sh_count(const ShSet& set, uint32_t j, bool prom
 // Builds the set of columns [c0, c0 + cols) from the history of `last`, the
 // chain's last row, with the words of `first`, its first.  Called by the whole
 // CTA.  `clean`: member is zero and nothing is in use.  Returns the number of
-// members; above SH_SET nothing but `member` is set.
+// members; above a.room nothing but `member` is set.
 __device__ int sh_build(const ShapeArgs& a, const ShSet& set, const ShRow& first, const ShRow& last, int c0, int cols,
                         bool clean, int* warp_sum) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -399,7 +399,7 @@ __device__ int sh_build(const ShapeArgs& a, const ShSet& set, const ShRow& first
     if (w < warp) off += warp_sum[w];
     total += warp_sum[w];
   }
-  if (total > SH_SET) return total;
+  if (total > a.room) return total;
   for (int i = i0; i < i1; ++i) {
     set.before[i] = static_cast<uint16_t>(off);
     for (uint32_t m = set.member[i]; m; m &= m - 1) set.col[off++] = static_cast<uint16_t>(i * 32 + __ffs(m) - 1);
@@ -467,8 +467,8 @@ __global__ void __launch_bounds__(SH_THREADS, OUT_TILE ? 3 : SH_CTAS) shape_kern
   ShSet set;
   set.member = reinterpret_cast<uint32_t*>(sh_smem);
   set.word = set.member + a.cols / 32;
-  set.col = reinterpret_cast<uint16_t*>(set.word + SH_SET);
-  set.before = set.col + SH_SET;
+  set.col = reinterpret_cast<uint16_t*>(set.word + a.room);
+  set.before = set.col + a.room;
   uint8_t* const tiles = reinterpret_cast<uint8_t*>(set.before + a.cols / 32 + 8);
   uint8_t* const ring = tiles + warp * (SH_STAGES * SH_TILE);
   uint8_t* const out_tile = tiles + SH_WARPS * (SH_STAGES * SH_TILE) + warp * SH_TILE;
@@ -656,10 +656,10 @@ __global__ void __launch_bounds__(SH_THREADS, OUT_TILE ? 3 : SH_CTAS) shape_kern
       if (ranked) {
         int members = sh_build(a, set, rows[head], rows[last], c0, cols, clean, warp_sum);
         clean = false;
-        while (members > SH_SET) {
-          // a share of the columns that should hold SH_SET of these members, or SH_SET columns, which do
-          const int64_t fit = static_cast<int64_t>(cols) * SH_SET / members * 4 / 5 / 1024 * 1024;
-          width = cols = width == cols && fit > SH_SET ? static_cast<int>(fit) : SH_SET;
+        while (members > a.room) {
+          // a share of the columns that should hold a.room of these members, or a.room columns, which do
+          const int64_t fit = static_cast<int64_t>(cols) * a.room / members * 4 / 5 / 1024 * 1024;
+          width = cols = width == cols && fit > a.room ? static_cast<int>(fit) : a.room;
           nseg = (cols + S::COLS - 1) / S::COLS;
           sh_copy_wait<0>();
           __syncwarp();
@@ -1020,11 +1020,18 @@ __global__ void __launch_bounds__(256) shaped_merge_kernel(const ShapeArgs a) {
   }
 }
 
+constexpr int sh_set_bytes(int cols, int room) { return cols / 32 * 6 + 16 + room * 6; }
+// members that a set of `cols` columns has room for: whole segments of either type, at most all columns
+constexpr int sh_room(int cols) {
+  const int room = (SH_SET_BYTES - sh_set_bytes(cols, 0)) / 6 / 1024 * 1024;
+  return room < cols ? room : cols;
+}
+static_assert(sh_room(SH_MAX_COLS) == 2048 && sh_room(3072) == 3072 && 1024 % SHAPE_MIN_SEG == 0, "room of a set");
+
 template <class TIn, class TOut, int MODE, bool ALIGNED, bool OUT_TILE, bool MASKS>
 cudaError_t launch_typed(const ShapeArgs& a, cudaStream_t st) {
-  const auto bytes = [](size_t cols) {
-    return cols / 32 * 6 + 16 + SH_SET * 6 + SH_WARPS * (SH_STAGES + (OUT_TILE ? 1 : 0)) * SH_TILE;
-  };
+  constexpr size_t TILES = SH_WARPS * (SH_STAGES + (OUT_TILE ? 1 : 0)) * SH_TILE;
+  const size_t smem = sh_set_bytes(a.cols, a.room) + TILES;
   const auto kernel = shape_kernel<TIn, TOut, MODE, ALIGNED, OUT_TILE, MASKS>;
   static std::atomic<uint64_t> ready{0};  // a bit per device whose limit is set
   int dev = 0;
@@ -1032,12 +1039,12 @@ cudaError_t launch_typed(const ShapeArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
   if (!(ready.load() & bit)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes(SH_MAX_COLS)));
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SH_SET_BYTES + TILES));
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit);
   }
   const int64_t blocks = static_cast<int64_t>(a.ntiles) * ceil_div(a.R, a.rows_per_cta);
-  kernel<<<static_cast<unsigned>(blocks), SH_THREADS, bytes(a.cols), st>>>(a);
+  kernel<<<static_cast<unsigned>(blocks), SH_THREADS, smem, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -1075,7 +1082,7 @@ void plan(ShapeArgs& a) {
     const int64_t cols = ceil_div(ceil_div(a.V, tiles), 1024) * 1024;
     const int64_t n = ceil_div(a.V, cols);
     const int64_t cost = ceil_div(a.R * n, slots) * (ceil_div(ceil_div(cols, seg), SH_WARPS) + 4);
-    if (best < 0 || cost < best) {
+    if (best < 0 || cost <= best) {  // more ranges of the same cost: fewer members each
       best = cost;
       a.cols = static_cast<int>(cols);
       a.ntiles = static_cast<int>(n);
@@ -1084,6 +1091,7 @@ void plan(ShapeArgs& a) {
   }
   const int64_t rows = static_cast<int64_t>(a.R) * a.ntiles / (8 * slots);
   a.rows_per_cta = static_cast<int>(rows < 1 ? 1 : (rows > SH_MAX_ROWS ? SH_MAX_ROWS : rows));
+  a.room = sh_room(a.cols);
   a.nseg = static_cast<int>(ceil_div(a.V, seg));
   const size_t in_elt = a.dtype == GH_BF16 ? 2 : 4, out_elt = a.out_dtype == GH_BF16 ? 2 : 4;
   a.vec_in = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && a.ld * in_elt % 16 == 0;
