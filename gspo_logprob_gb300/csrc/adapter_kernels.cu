@@ -19,7 +19,7 @@
 
 #include <mutex>
 
-#include "internal.h"
+#include "rollout.h"
 #include "tc_gemm.cuh"
 #include "tc_gemm_pair.cuh"
 

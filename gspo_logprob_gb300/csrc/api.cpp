@@ -15,6 +15,7 @@
 
 #include "grpo_head.h"
 #include "internal.h"
+#include "rollout.h"
 
 namespace gh {
 

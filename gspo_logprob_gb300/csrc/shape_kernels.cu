@@ -58,8 +58,8 @@
 
 #include <atomic>
 
-#include "internal.h"
 #include "ptx.cuh"
+#include "rollout.h"
 
 namespace gh {
 namespace {
