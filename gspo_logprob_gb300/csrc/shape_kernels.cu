@@ -670,301 +670,303 @@ __global__ void __launch_bounds__(SH_THREADS, OUT_TILE ? 3 : SH_CTAS) shape_kern
 
       int stage = 0;  // of the present segment
       for (uint32_t left = warp < nseg ? chain : 0u; left; left &= left - 1) {
-      const int rr = __ffs(left) - 1, row = row0 + rr;
-      const ShRow& r = rows[rr];
-      const int allow = MASKS ? r.allow : -1;
-      // the target, as a column of this range, and its segment
-      const int y = MODE != SHAPE_OUT && r.y >= c0 && r.y < c0 + cols ? r.y - c0 : -1;
-      const int ysg = y < 0 ? -1 : y / S::COLS;
-      float2* const part = MODE == SHAPE_LOGP ? a.part + static_cast<size_t>(row) * a.nseg + c0 / S::COLS : nullptr;
-      const float inv_t = r.inv_t, lse = r.lse, scale = r.scale;
-      const ShPen pen{r.rep, r.inv_rep, r.pres, r.freq, a.s.bias_values + (r.bias_b - 1)};
-      if (rr != head && (r.tab == TAB_ADD1 || r.tab == TAB_ADD)) {
-        // the row's new tokens among this warp's columns
-        const bool one = r.tab == TAB_ADD1;
-        for (int k = (one ? r.len - 1 : r.add) + lane; k < r.len; k += 32) {
-          const uint32_t j = static_cast<uint32_t>((one ? r.add : a.s.tokens[r.begin + k]) - c0);
-          if (j < static_cast<uint32_t>(cols) && static_cast<int>(j / S::COLS) % SH_WARPS == warp)
-            sh_count(set, j, k < r.plen);
+        const int rr = __ffs(left) - 1, row = row0 + rr;
+        const ShRow& r = rows[rr];
+        const int allow = MASKS ? r.allow : -1;
+        // the target, as a column of this range, and its segment
+        const int y = MODE != SHAPE_OUT && r.y >= c0 && r.y < c0 + cols ? r.y - c0 : -1;
+        const int ysg = y < 0 ? -1 : y / S::COLS;
+        float2* const part = MODE == SHAPE_LOGP ? a.part + static_cast<size_t>(row) * a.nseg + c0 / S::COLS : nullptr;
+        const float inv_t = r.inv_t, lse = r.lse, scale = r.scale;
+        const ShPen pen{r.rep, r.inv_rep, r.pres, r.freq, a.s.bias_values + (r.bias_b - 1)};
+        if (rr != head && (r.tab == TAB_ADD1 || r.tab == TAB_ADD)) {
+          // the row's new tokens among this warp's columns
+          const bool one = r.tab == TAB_ADD1;
+          for (int k = (one ? r.len - 1 : r.add) + lane; k < r.len; k += 32) {
+            const uint32_t j = static_cast<uint32_t>((one ? r.add : a.s.tokens[r.begin + k]) - c0);
+            if (j < static_cast<uint32_t>(cols) && static_cast<int>(j / S::COLS) % SH_WARPS == warp)
+              sh_count(set, j, k < r.plen);
+          }
+          __syncwarp();
         }
-        __syncwarp();
-      }
-      for (int sg = warp; sg < nseg; sg += SH_WARPS) {
-        const int seg = sg * S::COLS;
-        sh_copy_wait<SH_STAGES - 2>();
-        __syncwarp();  // every lane's part has landed, and the stage before is read
-        copy(oks[SH_STAGES - 1], ring + stage_c * SH_TILE);
-        if (left_c) next_c();
-        const uint32_t okw = oks[0];
+        for (int sg = warp; sg < nseg; sg += SH_WARPS) {
+          const int seg = sg * S::COLS;
+          sh_copy_wait<SH_STAGES - 2>();
+          __syncwarp();  // every lane's part has landed, and the stage before is read
+          copy(oks[SH_STAGES - 1], ring + stage_c * SH_TILE);
+          if (left_c) next_c();
+          const uint32_t okw = oks[0];
 #pragma unroll
-        for (int k = 0; k < SH_STAGES - 1; ++k) oks[k] = oks[k + 1];
-        oks[SH_STAGES - 1] = load_ok();
-        const bool whole = seg + S::COLS <= cols;
-        uint8_t* const buf = ring + stage * SH_TILE;
-        stage = stage == SH_STAGES - 1 ? 0 : stage + 1;
-        stage_c = stage_c == SH_STAGES - 1 ? 0 : stage_c + 1;
-        const int shift = ALIGNED ? 0
-                                  : static_cast<int>(reinterpret_cast<uintptr_t>(
-                                        first_byte + (static_cast<size_t>(row) * a.ld + (c0 + seg)) * sizeof(TIn)) & 15);
-        TIn* const x = reinterpret_cast<TIn*>(buf + shift);  // the segment's columns
+          for (int k = 0; k < SH_STAGES - 1; ++k) oks[k] = oks[k + 1];
+          oks[SH_STAGES - 1] = load_ok();
+          const bool whole = seg + S::COLS <= cols;
+          uint8_t* const buf = ring + stage * SH_TILE;
+          stage = stage == SH_STAGES - 1 ? 0 : stage + 1;
+          stage_c = stage_c == SH_STAGES - 1 ? 0 : stage_c + 1;
+          const uint8_t* const place = first_byte + (static_cast<size_t>(row) * a.ld + (c0 + seg)) * sizeof(TIn);
+          const int shift = ALIGNED ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(place) & 15);
+          TIn* const x = reinterpret_cast<TIn*>(buf + shift);  // the segment's columns
 
-        // members of the segment, by rank: a lane each, in as many rounds as it takes
-        int r0 = 0, r1 = 0;
-        if (ranked) {
-          r0 = set.before[sg * S::WORDS];
-          r1 = set.before[min((sg + 1) * S::WORDS, (cols + 31) >> 5)];
-        }
-        const bool masked = MASKS && allow >= 0;
-        const uint32_t* const allow_row = masked ? a.s.allow_bits + allow * allow_ld + (c0 >> 5) : nullptr;
-        const auto allowed = [&](int j) { return !masked || ((__ldg(allow_row + (j >> 5)) >> (j & 31)) & 1u) != 0; };
-        // a mask that leaves at most SH_FEW of any 32 columns: the sparse way costs less than the dense pass
-        const bool few = masked && __reduce_max_sync(0xffffffffu, __popc(okw)) <= SH_FEW;
+          // members of the segment, by rank: a lane each, in as many rounds as it takes
+          int r0 = 0, r1 = 0;
+          if (ranked) {
+            r0 = set.before[sg * S::WORDS];
+            r1 = set.before[min((sg + 1) * S::WORDS, (cols + 31) >> 5)];
+          }
+          const bool masked = MASKS && allow >= 0;
+          const uint32_t* const allow_row = masked ? a.s.allow_bits + allow * allow_ld + (c0 >> 5) : nullptr;
+          const auto allowed = [&](int j) { return !masked || ((__ldg(allow_row + (j >> 5)) >> (j & 31)) & 1u) != 0; };
+          // a mask that leaves at most SH_FEW of any 32 columns: the sparse way costs less than the dense pass
+          const bool few = masked && __reduce_max_sync(0xffffffffu, __popc(okw)) <= SH_FEW;
 
-        if (MODE == SHAPE_LOGP) {
-          if (sg == ysg) {
-            // the target, before the members' places change
-            if (lane == 0) {
-              float z = -INFINITY;
-              if (allowed(y)) {
-                const bool member = ranked && ((set.member[static_cast<uint32_t>(y) >> 5] >> (y & 31)) & 1u) != 0;
+          if (MODE == SHAPE_LOGP) {
+            if (sg == ysg) {
+              // the target, before the members' places change
+              if (lane == 0) {
+                float z = -INFINITY;
+                if (allowed(y)) {
+                  const bool member = ranked && ((set.member[static_cast<uint32_t>(y) >> 5] >> (y & 31)) & 1u) != 0;
+                  float slope;
+                  const uint32_t w = member ? set.word[set.rank(static_cast<uint32_t>(y))] : 0u;
+                  z = sh_member(pen, w, sh_to_float<TIn>(x[y - seg]), slope) * inv_t;
+                }
+                a.zy[row] = z;
+              }
+              __syncwarp();
+            }
+            // members: their exponentials go into a sum of integers (units of 2^-26 of the largest), which does not
+            // depend on the order, as ranks depend on the rows of the chain; their staged places get -inf
+            float zm = -INFINITY;
+            uint32_t fixed = 0;
+            bool nan = false;
+            if (r1 > r0) {
+              // rank q's shaped value and column (lanes past the last rank: -inf and -1); no branches
+              const auto value = [&](int q, int& at) {
+                const uint32_t w = q < r1 ? set.word[q] : 0u;
+                const int j = set.col[min(q, r1 - 1)];
                 float slope;
-                z = sh_member(pen, member ? set.word[set.rank(static_cast<uint32_t>(y))] : 0u, sh_to_float<TIn>(x[y - seg]), slope) * inv_t;
-              }
-              a.zy[row] = z;
-            }
-            __syncwarp();
-          }
-          // members: their exponentials go into a sum of integers (units of 2^-26 of the largest), which does not depend
-          // on the order, as ranks depend on the rows of the chain; their staged places get -inf
-          float zm = -INFINITY;
-          uint32_t fixed = 0;
-          bool nan = false;
-          if (r1 > r0) {
-            // rank q's shaped value and column (lanes past the last rank: -inf and -1); no branches
-            const auto value = [&](int q, int& at) {
-              const uint32_t w = q < r1 ? set.word[q] : 0u;
-              const int j = set.col[min(q, r1 - 1)];
-              float slope;
-              const float z = sh_member(pen, w, sh_to_float<TIn>(x[j - seg]), slope) * inv_t;
-              at = w ? j : -1;
-              return w && allowed(j) ? z : -INFINITY;
-            };
-            const auto add = [&](float z, int j) {
-              const float e = ex2_approx((z - zm) * SH_LOG2E);
-              nan |= e != e;
-              fixed += __float2uint_rn(e * SH_ONE);
-              if (j >= 0) x[j - seg] = sh_from_float<TIn>(-INFINITY);
-            };
-            int j0 = -1, j;
-            const float z0 = value(r0 + lane, j0);
-            zm = z0;
-            if (r1 - r0 > 32)
-              for (int q = r0 + 32 + lane; q < r1; q += 32) zm = fmaxf(zm, value(q, j));
-            zm = fmaxf(sh_warp_max(zm), -SH_LOWEST);  // the lowest finite value in place of -inf
-            add(z0, j0);
-            if (r1 - r0 > 32)
-              for (int q = r0 + 32 + lane; q < r1; q += 32) {
-                const float z = value(q, j);
-                add(z, j);
-              }
-            __syncwarp();
-          }
-          float m = -INFINITY, sum = 0.f, ml = -INFINITY, sl = 0.f;
-          ShRaw<TIn> raw[S::CHUNKS];
-          if (few) {
-            for (uint32_t v = okw; v; v &= v - 1) {
-              const float z = sh_to_float<TIn>(x[lane * 32 + __ffs(v) - 1]) * inv_t;
-              const float mn = fmaxf(fmaxf(ml, z), -SH_LOWEST);
-              sl = sl * ex2_approx((ml - mn) * SH_LOG2E) + ex2_approx((z - mn) * SH_LOG2E);
-              ml = mn;
-            }
-            m = ml;
-          } else {
-            if (masked || !whole) {
-              // barred columns to -inf, in the stage
-              const uint32_t ok = bytes_of(okw);
-#pragma unroll
-              for (int u = 0; u < S::CHUNKS; ++u) {
-                const uint32_t bar = ((ok >> (8 * u)) & 0xffu) ^ 0xffu;
-                if (shift == 0) {
-                  sh_read<ShRaw<TIn>::N>(raw[u].w, buf + u * CB + lane * 16 * S::LANE16, 0);
-                  sh_fill(raw[u], bar, sh_minus_inf<TIn>());
-#pragma unroll
-                  for (int q = 0; q < ShRaw<TIn>::N / 4; ++q)
-                    *(reinterpret_cast<uint4*>(buf + u * CB + lane * 16 * S::LANE16) + q) =
-                        make_uint4(raw[u].w[4 * q], raw[u].w[4 * q + 1], raw[u].w[4 * q + 2], raw[u].w[4 * q + 3]);
-                } else {
-                  for (uint32_t v = bar; v; v &= v - 1) x[u * 256 + lane * 8 + __ffs(v) - 1] = sh_from_float<TIn>(-INFINITY);
+                const float z = sh_member(pen, w, sh_to_float<TIn>(x[j - seg]), slope) * inv_t;
+                at = w ? j : -1;
+                return w && allowed(j) ? z : -INFINITY;
+              };
+              const auto add = [&](float z, int j) {
+                const float e = ex2_approx((z - zm) * SH_LOG2E);
+                nan |= e != e;
+                fixed += __float2uint_rn(e * SH_ONE);
+                if (j >= 0) x[j - seg] = sh_from_float<TIn>(-INFINITY);
+              };
+              int j0 = -1, j;
+              const float z0 = value(r0 + lane, j0);
+              zm = z0;
+              if (r1 - r0 > 32)
+                for (int q = r0 + 32 + lane; q < r1; q += 32) zm = fmaxf(zm, value(q, j));
+              zm = fmaxf(sh_warp_max(zm), -SH_LOWEST);  // the lowest finite value in place of -inf
+              add(z0, j0);
+              if (r1 - r0 > 32)
+                for (int q = r0 + 32 + lane; q < r1; q += 32) {
+                  const float z = value(q, j);
+                  add(z, j);
                 }
-              }
               __syncwarp();
             }
-#pragma unroll
-            for (int u = 0; u < S::CHUNKS; ++u) sh_read<ShRaw<TIn>::N>(raw[u].w, buf + u * CB + lane * 16 * S::LANE16, shift);
-            if constexpr (sizeof(TIn) == 2) {
-              __nv_bfloat162 h[S::CHUNKS * 4];
-#pragma unroll
-              for (int u = 0; u < S::CHUNKS; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) h[u * 4 + i] = *reinterpret_cast<const __nv_bfloat162*>(&raw[u].w[i]);
-#pragma unroll
-              for (int o = S::CHUNKS * 2; o > 0; o >>= 1)
-#pragma unroll
-                for (int i = 0; i < o; ++i) h[i] = __hmax2(h[i], h[i + o]);
-              m = fmaxf(__low2float(h[0]), __high2float(h[0]));
-            } else {
-#pragma unroll
-              for (int u = 0; u < S::CHUNKS; ++u)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) m = fmaxf(m, __uint_as_float(raw[u].w[i]));
-            }
-            m *= inv_t;  // 1 / T > 0: the maximum of the raw values is that of the scaled ones
-          }
-          m = fmaxf(sh_warp_max(m), zm);
-          const float ref = fmaxf(m, -SH_LOWEST);
-          if (few) {
-            sum = sl * ex2_approx((ml - ref) * SH_LOG2E);
-          } else if (fabsf(ref) < SH_BIG) {
-            float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            const float k = inv_t * SH_LOG2E, c = -ref * SH_LOG2E;
-            const float2 k2 = make_float2(k, k), c2 = make_float2(c, c);
-#pragma unroll
-            for (int u = 0; u < S::CHUNKS; ++u)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float2 v = sh_fma2(sh_pair(raw[u], i), k2, c2);
-                acc[i & 1] = sh_add2(acc[i & 1], make_float2(ex2_approx(v.x), ex2_approx(v.y)));
-              }
-            sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-          } else {  // values near the type's lowest: the difference first
-#pragma unroll 1
-            for (int u = 0; u < S::CHUNKS; ++u) {
-              sh_read<ShRaw<TIn>::N>(raw[0].w, buf + u * CB + lane * 16 * S::LANE16, shift);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float2 v = sh_pair(raw[0], i);
-                sum += ex2_approx(fmaf(v.x, inv_t, -ref) * SH_LOG2E);
-                sum += ex2_approx(fmaf(v.y, inv_t, -ref) * SH_LOG2E);
-              }
-            }
-          }
-          if (nan) sum = __int_as_float(0x7fc00000);
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          if (r1 > r0) {
-            // a lane has at most 32 members: below 2^32; so have 32 lanes one each
-            float t;
-            if (r1 - r0 <= 32)
-              t = static_cast<float>(__reduce_add_sync(0xffffffffu, fixed));
-            else
-              t = fmaf(static_cast<float>(__reduce_add_sync(0xffffffffu, fixed >> 16)), 65536.f,
-                       static_cast<float>(__reduce_add_sync(0xffffffffu, fixed & 0xffffu)));
-            sum += t * (1.f / SH_ONE) * ex2_approx((zm - ref) * SH_LOG2E);
-          }
-          if (lane == 0) part[sg] = make_float2(m, sum);
-        } else {
-          TOut* const out = reinterpret_cast<TOut*>(a.out) + static_cast<size_t>(row) * a.out_ld + (c0 + seg);
-          const uint32_t bars = masked ? bytes_of(okw) ^ S::FULL : 0u;
-          const bool small = fabsf(lse) < SH_BIG;
-          const float k = MODE == SHAPE_OUT ? inv_t : inv_t * SH_LOG2E, c = -lse * SH_LOG2E;
-          const float2 k2 = make_float2(k, k), c2 = make_float2(c, c), g2 = make_float2(-scale, -scale);
-#pragma unroll
-          for (int u = 0; u < S::CHUNKS; ++u) {
-            ShRaw<TOut> o;
+            float m = -INFINITY, sum = 0.f, ml = -INFINITY, sl = 0.f;
+            ShRaw<TIn> raw[S::CHUNKS];
             if (few) {
-#pragma unroll
-              for (int i = 0; i < ShRaw<TOut>::N; ++i) o.w[i] = MODE == SHAPE_OUT ? sh_minus_inf<TOut>() : 0u;
+              for (uint32_t v = okw; v; v &= v - 1) {
+                const float z = sh_to_float<TIn>(x[lane * 32 + __ffs(v) - 1]) * inv_t;
+                const float mn = fmaxf(fmaxf(ml, z), -SH_LOWEST);
+                sl = sl * ex2_approx((ml - mn) * SH_LOG2E) + ex2_approx((z - mn) * SH_LOG2E);
+                ml = mn;
+              }
+              m = ml;
             } else {
-              ShRaw<TIn> raw;
-              sh_read<ShRaw<TIn>::N>(raw.w, buf + u * CB + lane * 16 * S::LANE16, shift);
+              if (masked || !whole) {
+                // barred columns to -inf, in the stage
+                const uint32_t ok = bytes_of(okw);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                float2 v = sh_pair(raw, i);
-                if (MODE == SHAPE_OUT) {
-                  v = sh_mul2(v, k2);
-                } else {
-                  if (small) {
-                    v = sh_fma2(v, k2, c2);
-                  } else {  // the difference first
-                    v.x = fmaf(v.x, inv_t, -lse) * SH_LOG2E;
-                    v.y = fmaf(v.y, inv_t, -lse) * SH_LOG2E;
+                for (int u = 0; u < S::CHUNKS; ++u) {
+                  const uint32_t bar = ((ok >> (8 * u)) & 0xffu) ^ 0xffu;
+                  if (shift == 0) {
+                    sh_read<ShRaw<TIn>::N>(raw[u].w, buf + u * CB + lane * 16 * S::LANE16, 0);
+                    sh_fill(raw[u], bar, sh_minus_inf<TIn>());
+#pragma unroll
+                    for (int q = 0; q < ShRaw<TIn>::N / 4; ++q)
+                      *(reinterpret_cast<uint4*>(buf + u * CB + lane * 16 * S::LANE16) + q) =
+                          make_uint4(raw[u].w[4 * q], raw[u].w[4 * q + 1], raw[u].w[4 * q + 2], raw[u].w[4 * q + 3]);
+                  } else {
+                    for (uint32_t v = bar; v; v &= v - 1)
+                      x[u * 256 + lane * 8 + __ffs(v) - 1] = sh_from_float<TIn>(-INFINITY);
                   }
-                  v = sh_mul2(make_float2(ex2_approx(v.x), ex2_approx(v.y)), g2);
                 }
-                sh_put(o, i, v);
+                __syncwarp();
               }
-              if (masked) sh_fill(o, (bars >> (8 * u)) & 0xffu, MODE == SHAPE_OUT ? sh_minus_inf<TOut>() : 0u);
-            }
-            const int j = u * 256 + lane * 8, n = cols - seg - j;
-            if (OUT_TILE) {
 #pragma unroll
-              for (int q = 0; q < ShRaw<TOut>::N / 4; ++q)
-                *(reinterpret_cast<uint4*>(out_tile + j * sizeof(TOut)) + q) =
-                    make_uint4(o.w[4 * q], o.w[4 * q + 1], o.w[4 * q + 2], o.w[4 * q + 3]);
-            } else if (a.vec_out && (whole || n >= 8)) {
+              for (int u = 0; u < S::CHUNKS; ++u)
+                sh_read<ShRaw<TIn>::N>(raw[u].w, buf + u * CB + lane * 16 * S::LANE16, shift);
+              if constexpr (sizeof(TIn) == 2) {
+                __nv_bfloat162 h[S::CHUNKS * 4];
 #pragma unroll
-              for (int q = 0; q < ShRaw<TOut>::N / 4; ++q)
-                __stcs(reinterpret_cast<uint4*>(out + j) + q,
-                       make_uint4(o.w[4 * q], o.w[4 * q + 1], o.w[4 * q + 2], o.w[4 * q + 3]));
-            } else {
+                for (int u = 0; u < S::CHUNKS; ++u)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float2 v = sh_pair(o, i);
-                if (2 * i < n) out[j + 2 * i] = sh_from_float<TOut>(v.x);
-                if (2 * i + 1 < n) out[j + 2 * i + 1] = sh_from_float<TOut>(v.y);
-              }
-            }
-          }
-          const bool here = MODE == SHAPE_GRAD && sg == ysg;
-          if (few || r1 > r0 || here) {
-            __syncwarp();  // after the dense stores of the other lanes
-            TOut* const to = OUT_TILE ? reinterpret_cast<TOut*>(out_tile) : out;
-            // column j of the segment with a member's word, or 0
-            const auto put = [&](int j, uint32_t w) {
-              float slope;
-              const float z = sh_member(pen, w, sh_to_float<TIn>(x[j]), slope);
-              float v;
-              if (MODE == SHAPE_OUT) {
-                v = z * inv_t;
+                  for (int i = 0; i < 4; ++i) h[u * 4 + i] = *reinterpret_cast<const __nv_bfloat162*>(&raw[u].w[i]);
+#pragma unroll
+                for (int o = S::CHUNKS * 2; o > 0; o >>= 1)
+#pragma unroll
+                  for (int i = 0; i < o; ++i) h[i] = __hmax2(h[i], h[i + o]);
+                m = fmaxf(__low2float(h[0]), __high2float(h[0]));
               } else {
-                const float p = ex2_approx(fmaf(z, inv_t, -lse) * SH_LOG2E);
-                v = scale * slope * ((j + seg == y ? 1.f : 0.f) - p);
+#pragma unroll
+                for (int u = 0; u < S::CHUNKS; ++u)
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) m = fmaxf(m, __uint_as_float(raw[u].w[i]));
               }
-              to[j] = sh_from_float<TOut>(v);
-            };
+              m *= inv_t;  // 1 / T > 0: the maximum of the raw values is that of the scaled ones
+            }
+            m = fmaxf(sh_warp_max(m), zm);
+            const float ref = fmaxf(m, -SH_LOWEST);
             if (few) {
-              for (uint32_t v = okw; v; v &= v - 1) put(lane * 32 + __ffs(v) - 1, 0u);
+              sum = sl * ex2_approx((ml - ref) * SH_LOG2E);
+            } else if (fabsf(ref) < SH_BIG) {
+              float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+              const float k = inv_t * SH_LOG2E, c = -ref * SH_LOG2E;
+              const float2 k2 = make_float2(k, k), c2 = make_float2(c, c);
+#pragma unroll
+              for (int u = 0; u < S::CHUNKS; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float2 v = sh_fma2(sh_pair(raw[u], i), k2, c2);
+                  acc[i & 1] = sh_add2(acc[i & 1], make_float2(ex2_approx(v.x), ex2_approx(v.y)));
+                }
+              sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+            } else {  // values near the type's lowest: the difference first
+#pragma unroll 1
+              for (int u = 0; u < S::CHUNKS; ++u) {
+                sh_read<ShRaw<TIn>::N>(raw[0].w, buf + u * CB + lane * 16 * S::LANE16, shift);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float2 v = sh_pair(raw[0], i);
+                  sum += ex2_approx(fmaf(v.x, inv_t, -ref) * SH_LOG2E);
+                  sum += ex2_approx(fmaf(v.y, inv_t, -ref) * SH_LOG2E);
+                }
+              }
+            }
+            if (nan) sum = __int_as_float(0x7fc00000);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (r1 > r0) {
+              // a lane has at most 32 members: below 2^32; so have 32 lanes one each
+              float t;
+              if (r1 - r0 <= 32)
+                t = static_cast<float>(__reduce_add_sync(0xffffffffu, fixed));
+              else
+                t = fmaf(static_cast<float>(__reduce_add_sync(0xffffffffu, fixed >> 16)), 65536.f,
+                         static_cast<float>(__reduce_add_sync(0xffffffffu, fixed & 0xffffu)));
+              sum += t * (1.f / SH_ONE) * ex2_approx((zm - ref) * SH_LOG2E);
+            }
+            if (lane == 0) part[sg] = make_float2(m, sum);
+          } else {
+            TOut* const out = reinterpret_cast<TOut*>(a.out) + static_cast<size_t>(row) * a.out_ld + (c0 + seg);
+            const uint32_t bars = masked ? bytes_of(okw) ^ S::FULL : 0u;
+            const bool small = fabsf(lse) < SH_BIG;
+            const float k = MODE == SHAPE_OUT ? inv_t : inv_t * SH_LOG2E, c = -lse * SH_LOG2E;
+            const float2 k2 = make_float2(k, k), c2 = make_float2(c, c), g2 = make_float2(-scale, -scale);
+#pragma unroll
+            for (int u = 0; u < S::CHUNKS; ++u) {
+              ShRaw<TOut> o;
+              if (few) {
+#pragma unroll
+                for (int i = 0; i < ShRaw<TOut>::N; ++i) o.w[i] = MODE == SHAPE_OUT ? sh_minus_inf<TOut>() : 0u;
+              } else {
+                ShRaw<TIn> raw;
+                sh_read<ShRaw<TIn>::N>(raw.w, buf + u * CB + lane * 16 * S::LANE16, shift);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  float2 v = sh_pair(raw, i);
+                  if (MODE == SHAPE_OUT) {
+                    v = sh_mul2(v, k2);
+                  } else {
+                    if (small) {
+                      v = sh_fma2(v, k2, c2);
+                    } else {  // the difference first
+                      v.x = fmaf(v.x, inv_t, -lse) * SH_LOG2E;
+                      v.y = fmaf(v.y, inv_t, -lse) * SH_LOG2E;
+                    }
+                    v = sh_mul2(make_float2(ex2_approx(v.x), ex2_approx(v.y)), g2);
+                  }
+                  sh_put(o, i, v);
+                }
+                if (masked) sh_fill(o, (bars >> (8 * u)) & 0xffu, MODE == SHAPE_OUT ? sh_minus_inf<TOut>() : 0u);
+              }
+              const int j = u * 256 + lane * 8, n = cols - seg - j;
+              if (OUT_TILE) {
+#pragma unroll
+                for (int q = 0; q < ShRaw<TOut>::N / 4; ++q)
+                  *(reinterpret_cast<uint4*>(out_tile + j * sizeof(TOut)) + q) =
+                      make_uint4(o.w[4 * q], o.w[4 * q + 1], o.w[4 * q + 2], o.w[4 * q + 3]);
+              } else if (a.vec_out && (whole || n >= 8)) {
+#pragma unroll
+                for (int q = 0; q < ShRaw<TOut>::N / 4; ++q)
+                  __stcs(reinterpret_cast<uint4*>(out + j) + q,
+                         make_uint4(o.w[4 * q], o.w[4 * q + 1], o.w[4 * q + 2], o.w[4 * q + 3]));
+              } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float2 v = sh_pair(o, i);
+                  if (2 * i < n) out[j + 2 * i] = sh_from_float<TOut>(v.x);
+                  if (2 * i + 1 < n) out[j + 2 * i + 1] = sh_from_float<TOut>(v.y);
+                }
+              }
+            }
+            const bool here = MODE == SHAPE_GRAD && sg == ysg;
+            if (few || r1 > r0 || here) {
+              __syncwarp();  // after the dense stores of the other lanes
+              TOut* const to = OUT_TILE ? reinterpret_cast<TOut*>(out_tile) : out;
+              // column j of the segment with a member's word, or 0
+              const auto put = [&](int j, uint32_t w) {
+                float slope;
+                const float z = sh_member(pen, w, sh_to_float<TIn>(x[j]), slope);
+                float v;
+                if (MODE == SHAPE_OUT) {
+                  v = z * inv_t;
+                } else {
+                  const float p = ex2_approx(fmaf(z, inv_t, -lse) * SH_LOG2E);
+                  v = scale * slope * ((j + seg == y ? 1.f : 0.f) - p);
+                }
+                to[j] = sh_from_float<TOut>(v);
+              };
+              if (few) {
+                for (uint32_t v = okw; v; v &= v - 1) put(lane * 32 + __ffs(v) - 1, 0u);
+                __syncwarp();
+              } else if (here) {
+                if (lane == 0 && allowed(y)) put(y - seg, 0u);
+                __syncwarp();
+              }
+              for (int q = r0 + lane; q < r1; q += 32) {
+                const uint32_t w = set.word[q];
+                const int j = set.col[q];
+                if (w && allowed(j)) put(j - seg, w);
+              }
+            }
+            if (OUT_TILE) {
               __syncwarp();
-            } else if (here) {
-              if (lane == 0 && allowed(y)) put(y - seg, 0u);
-              __syncwarp();
+              // 16-byte words of the output, and the elements before and after them
+              const int n = min(cols - seg, S::COLS);
+              const uintptr_t b = reinterpret_cast<uintptr_t>(out), e = b + n * sizeof(TOut);
+              const int before = min(static_cast<int>(((16 - (b & 15)) & 15) / sizeof(TOut)), n);
+              const int words = static_cast<int>((e - (b + before * sizeof(TOut))) / 16);
+              const int after = before + words * 16 / static_cast<int>(sizeof(TOut));
+              const TOut* src = reinterpret_cast<const TOut*>(out_tile);
+              if (lane < before) out[lane] = src[lane];
+              for (int q = lane; q < words; q += 32) {
+                uint32_t w[4];
+                sh_read<4>(w, out_tile + q * 16, before * static_cast<int>(sizeof(TOut)));
+                __stcs(reinterpret_cast<uint4*>(out + before) + q, make_uint4(w[0], w[1], w[2], w[3]));
+              }
+              if (lane < n - after) out[after + lane] = src[after + lane];
+              __syncwarp();  // the output tile is free
             }
-            for (int q = r0 + lane; q < r1; q += 32) {
-              const uint32_t w = set.word[q];
-              const int j = set.col[q];
-              if (w && allowed(j)) put(j - seg, w);
-            }
-          }
-          if (OUT_TILE) {
-            __syncwarp();
-            // 16-byte words of the output, and the elements before and after them
-            const int n = min(cols - seg, S::COLS);
-            const uintptr_t b = reinterpret_cast<uintptr_t>(out), e = b + n * sizeof(TOut);
-            const int before = min(static_cast<int>(((16 - (b & 15)) & 15) / sizeof(TOut)), n);
-            const int words = static_cast<int>((e - (b + before * sizeof(TOut))) / 16);
-            const int after = before + words * 16 / static_cast<int>(sizeof(TOut));
-            const TOut* src = reinterpret_cast<const TOut*>(out_tile);
-            if (lane < before) out[lane] = src[lane];
-            for (int q = lane; q < words; q += 32) {
-              uint32_t w[4];
-              sh_read<4>(w, out_tile + q * 16, before * static_cast<int>(sizeof(TOut)));
-              __stcs(reinterpret_cast<uint4*>(out + before) + q, make_uint4(w[0], w[1], w[2], w[3]));
-            }
-            if (lane < n - after) out[after + lane] = src[after + lane];
-            __syncwarp();  // the output tile is free
           }
         }
-      }
       }
       sh_copy_wait<0>();
       __syncwarp();  // the stages are free
