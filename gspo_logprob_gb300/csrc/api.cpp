@@ -896,8 +896,10 @@ gh_status grpo_shaped_logp(const gh_shaping* shaping, const void* logits, int32_
   a.lse_out = lse;
   cudaError_t e = run(K_SHAPED_LOGP, st, [&] { return launch_shaped_logp(a, st); });
   if (e != cudaSuccess) return cuda_fail(e, "shaped log-prob launch");
-  e = run(K_SHAPED_MERGE, st, [&] { return launch_shaped_merge(a, st); });
-  if (e != cudaSuccess) return cuda_fail(e, "shaped log-prob merge launch");
+  if (a.ntiles > 1) {
+    e = run(K_SHAPED_MERGE, st, [&] { return launch_shaped_merge(a, st); });
+    if (e != cudaSuccess) return cuda_fail(e, "shaped log-prob merge launch");
+  }
   return GH_OK;
 }
 

@@ -47,8 +47,9 @@ struct ShapeArgs {
 };
 int64_t shape_segments(int64_t V);
 cudaError_t launch_shape(ShapeArgs a, cudaStream_t st);
-cudaError_t launch_shaped_logp(ShapeArgs a, cudaStream_t st);   // segment partials and target logits
-cudaError_t launch_shaped_merge(ShapeArgs a, cudaStream_t st);  // logp and LSE from them
+// segment partials and target logits, and logp and LSE too where a.ntiles (which it sets) is 1
+cudaError_t launch_shaped_logp(ShapeArgs& a, cudaStream_t st);
+cudaError_t launch_shaped_merge(const ShapeArgs& a, cudaStream_t st);  // logp and LSE from them, after launch_shaped_logp
 cudaError_t launch_shaped_grad(ShapeArgs a, cudaStream_t st);
 
 // --- head with adapters (adapter_kernels.cu) -----------------------------------

@@ -56,6 +56,7 @@
 // instance runs.
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "ptx.cuh"
@@ -444,6 +445,51 @@ __device__ __forceinline__ float sh_member(const ShPen& p, uint32_t w, float x, 
   x = x * slope - (c ? fmaf(p.freq, static_cast<float>(c), p.pres) : 0.f);
   const uint32_t b = w >> SH_BIAS_SHIFT;
   return b ? x + __ldg(p.bias + b) : x;
+}
+
+// A warp folds a row's segment partials to its log-prob and LSE: lane l takes
+// segments l, l + 32, ... in order, then the lanes combine in a xor butterfly.
+__device__ __forceinline__ void sh_finish(const ShapeArgs& a, int row, int lane) {
+  if (a.mask[row] == 0) {
+    if (lane == 0) {
+      a.logp[row] = 0.f;
+      a.lse_out[row] = 0.f;
+    }
+    return;
+  }
+  float m = -INFINITY, s = 0.f;
+  const float2* p = a.part + static_cast<size_t>(row) * a.nseg;
+  for (int k = lane; k < a.nseg; k += 32) {
+    const float2 q = p[k];
+    const float mn = fmaxf(m, q.x);
+    const float ref = mn == -INFINITY ? 0.f : mn;
+    s = s * ex2_approx((m - ref) * SH_LOG2E) + q.y * ex2_approx((q.x - ref) * SH_LOG2E);
+    m = mn;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+    const float mn = fmaxf(m, m2);
+    const float ref = mn == -INFINITY ? 0.f : mn;
+    s = s * ex2_approx((m - ref) * SH_LOG2E) + s2 * ex2_approx((m2 - ref) * SH_LOG2E);
+    m = mn;
+  }
+  if (lane == 0) {
+    const int y = a.targets[row];
+    const float ls = logf(s);
+    const float lse = m + ls;  // -inf when the mask leaves nothing
+    float lp;
+    if (y >= 0 && y < a.V) {
+      const float z = a.zy[row];
+      lp = z == -INFINITY ? -INFINITY : (z - m) - ls;
+    } else {
+      lp = __int_as_float(0x7fc00000);
+      atomicOr(a.status, GH_DEV_TARGET_OOR);
+    }
+    a.logp[row] = lp;
+    a.lse_out[row] = lse;
+    if (!isfinite(lse) || (y >= 0 && y < a.V && !isfinite(lp))) atomicOr(a.status, GH_DEV_NONFINITE);
+  }
 }
 
 // Shared memory of a CTA: the set, then each warp's stages and (unaligned
@@ -972,54 +1018,18 @@ __global__ void __launch_bounds__(SH_THREADS, OUT_TILE ? 3 : SH_CTAS) shape_kern
       __syncwarp();  // the stages are free
     }
   }
+  if (MODE == SHAPE_LOGP && a.ntiles == 1) {
+    // all of these rows' partials are this CTA's: no second launch (1024 rows of 4096 columns: 15.5 -> 15.2 us of the
+    // device, 16.2 -> 15.4 of the host)
+    __syncthreads();
+    for (int rr = warp; rr < nrows; rr += SH_WARPS) sh_finish(a, row0 + rr, lane);
+  }
 }
 
-// A warp per row folds the row's segment partials: lane l takes segments l,
-// l + 32, ... in order, then the lanes combine in a xor butterfly.
+// A warp per row, where a row's columns are several CTAs'.
 __global__ void __launch_bounds__(256) shaped_merge_kernel(const ShapeArgs a) {
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= a.R) return;
-  if (a.mask[row] == 0) {
-    if (lane == 0) {
-      a.logp[row] = 0.f;
-      a.lse_out[row] = 0.f;
-    }
-    return;
-  }
-  float m = -INFINITY, s = 0.f;
-  const float2* p = a.part + static_cast<size_t>(row) * a.nseg;
-  for (int k = lane; k < a.nseg; k += 32) {
-    const float2 q = p[k];
-    const float mn = fmaxf(m, q.x);
-    const float ref = mn == -INFINITY ? 0.f : mn;
-    s = s * ex2_approx((m - ref) * SH_LOG2E) + q.y * ex2_approx((q.x - ref) * SH_LOG2E);
-    m = mn;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-    const float mn = fmaxf(m, m2);
-    const float ref = mn == -INFINITY ? 0.f : mn;
-    s = s * ex2_approx((m - ref) * SH_LOG2E) + s2 * ex2_approx((m2 - ref) * SH_LOG2E);
-    m = mn;
-  }
-  if (lane == 0) {
-    const int y = a.targets[row];
-    const float ls = logf(s);
-    const float lse = m + ls;  // -inf when the mask leaves nothing
-    float lp;
-    if (y >= 0 && y < a.V) {
-      const float z = a.zy[row];
-      lp = z == -INFINITY ? -INFINITY : (z - m) - ls;
-    } else {
-      lp = __int_as_float(0x7fc00000);
-      atomicOr(a.status, GH_DEV_TARGET_OOR);
-    }
-    a.logp[row] = lp;
-    a.lse_out[row] = lse;
-    if (!isfinite(lse) || (y >= 0 && y < a.V && !isfinite(lp))) atomicOr(a.status, GH_DEV_NONFINITE);
-  }
+  if (row < a.R) sh_finish(a, row, threadIdx.x & 31);
 }
 
 constexpr int sh_set_bytes(int cols, int room) { return cols / 32 * 6 + 16 + room * 6; }
@@ -1076,7 +1086,14 @@ cudaError_t launch_mode(const ShapeArgs& a, cudaStream_t st) {
 // 61 us.  Then as many rows per CTA as leave eight rounds: longer chains save set
 // builds, shorter ones even out rows that are not live (8192 rows of packed
 // sequences: 262 us with 4 rounds, 244 with 8, 261 with 16).
-void plan(ShapeArgs& a) {
+// Fewer rows than that, but more than a batch of requests: packed sequences, whose
+// rows share a set.  Two rows per CTA at least, and the log-prob, which the set-up
+// bounds more than the gradient, up to four while two rounds are left.  One row per
+// CTA -> this, us: log-prob 8192 x 32000 108 -> 76, 4096 x 32000 54 -> 44,
+// 1024 x 151936 66 -> 59, 1024 x 4096 15.5 -> 14; gradient 4096 x 32000 74 -> 69.
+// It would cost a batch of requests, whose rows share nothing, 5 to 10% (256 rows
+// of 151936: 44 -> 47; 1000 of 32000: 39 -> 43), hence the least number of rows.
+void plan(ShapeArgs& a, int mode) {
   const int64_t slots = static_cast<int64_t>(SH_CTAS) * num_sms();
   const int seg = a.dtype == GH_BF16 ? ShSeg<__nv_bfloat16>::COLS : ShSeg<float>::COLS;
   int64_t best = -1;
@@ -1084,14 +1101,20 @@ void plan(ShapeArgs& a) {
     const int64_t cols = ceil_div(ceil_div(a.V, tiles), 1024) * 1024;
     const int64_t n = ceil_div(a.V, cols);
     const int64_t cost = ceil_div(a.R * n, slots) * (ceil_div(ceil_div(cols, seg), SH_WARPS) + 4);
-    if (best < 0 || cost <= best) {  // more ranges of the same cost: fewer members each
+    // more ranges of the same cost: fewer members each, but a second launch for the log-prob
+    if (best < 0 || cost < best || (cost == best && !(mode == SHAPE_LOGP && a.ntiles == 1))) {
       best = cost;
       a.cols = static_cast<int>(cols);
       a.ntiles = static_cast<int>(n);
     }
     if (tiles > 64 && a.R * tiles > 8 * slots) break;  // more ranges only add rounds
   }
-  const int64_t rows = static_cast<int64_t>(a.R) * a.ntiles / (8 * slots);
+  const int64_t blocks = static_cast<int64_t>(a.R) * a.ntiles;
+  int64_t rows = blocks / (8 * slots);
+  if (mode != SHAPE_OUT && 5 * static_cast<int64_t>(a.R) >= 8 * slots) {
+    const int64_t least = mode == SHAPE_LOGP && blocks >= 4 * slots ? blocks / (2 * slots) : 2;
+    rows = std::max(rows, std::min<int64_t>(least, 4));
+  }
   a.rows_per_cta = static_cast<int>(rows < 1 ? 1 : (rows > SH_MAX_ROWS ? SH_MAX_ROWS : rows));
   a.room = sh_room(a.cols);
   a.nseg = static_cast<int>(ceil_div(a.V, seg));
@@ -1107,20 +1130,19 @@ int64_t shape_segments(int64_t V) { return ceil_div(V, SHAPE_MIN_SEG); }
 static_assert(SHAPE_MIN_SEG == ShSeg<float>::COLS && SHAPE_MIN_SEG <= ShSeg<__nv_bfloat16>::COLS, "workspace bound");
 
 cudaError_t launch_shape(ShapeArgs a, cudaStream_t st) {
-  plan(a);
+  plan(a, SHAPE_OUT);
   return launch_mode<SHAPE_OUT>(a, st);
 }
-cudaError_t launch_shaped_logp(ShapeArgs a, cudaStream_t st) {
-  plan(a);
+cudaError_t launch_shaped_logp(ShapeArgs& a, cudaStream_t st) {
+  plan(a, SHAPE_LOGP);
   return launch_mode<SHAPE_LOGP>(a, st);
 }
-cudaError_t launch_shaped_merge(ShapeArgs a, cudaStream_t st) {
-  plan(a);
+cudaError_t launch_shaped_merge(const ShapeArgs& a, cudaStream_t st) {
   shaped_merge_kernel<<<static_cast<unsigned>(ceil_div(a.R, 8)), 256, 0, st>>>(a);
   return cudaGetLastError();
 }
 cudaError_t launch_shaped_grad(ShapeArgs a, cudaStream_t st) {
-  plan(a);
+  plan(a, SHAPE_GRAD);
   return launch_mode<SHAPE_GRAD>(a, st);
 }
 

@@ -277,6 +277,32 @@ def test_bits_do_not_depend_on_the_batch_or_the_stride(gpu_lib):
             assert torch.equal(a, c[rows])
 
 
+@pytest.mark.parametrize("n,V,dtype", [(1024, 1000, "fp32"), (2100, 2049, "bf16"), (4001, 500, "bf16"),
+                                       (1030, 40000, "bf16")])
+def test_micro_batches_of_packed_sequences(gpu_lib, n, V, dtype):
+    # rows per CTA from two to four, whole rows per CTA (one launch) and ranges of them (two): the oracle's values,
+    # and the bits of rows that are called by themselves
+    import gspo_logprob_gb300 as g
+    rng = np.random.default_rng(n)
+    b = _batch(rng, n, V, features=("hist", "bias", "temp"), shared=True)
+    first = np.arange(n) // 97 * 97
+    b["hist_begin"] = first.astype(np.int64)
+    b["hist_len"] = (np.arange(n) - first).astype(np.int32)
+    b["prompt_len"] = np.full(n, 9, np.int32)
+    for k in ("repetition", "presence", "frequency", "temperature"):
+        b[k] = b[k][first]
+    y, m = _targets(rng, n, V)
+    x = _values(rng, n, V, dtype)
+    z, f, dz = _run_all(b, x, y, m, dtype)
+    for at, k in ((0, 1), (90, 20), (n - 30, 30)):
+        rows = slice(at, at + k)
+        sub = {q: (v[rows] if v.shape[:1] == (n,) and q != "tokens" else v) for q, v in b.items()}
+        fs = g.grpo_shaped_logp(_device(x[rows], dtype), torch.from_numpy(y[rows]).cuda(),
+                                torch.from_numpy(m[rows]).cuda(), _shaping(sub, k, V))
+        assert torch.equal(fs["logp"].view(torch.int32), f["logp"][rows].view(torch.int32))
+        assert torch.equal(fs["lse"].view(torch.int32), f["lse"][rows].view(torch.int32))
+
+
 def test_in_place(gpu_lib):
     import gspo_logprob_gb300 as g
     rng = np.random.default_rng(10)
