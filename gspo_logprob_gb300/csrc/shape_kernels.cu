@@ -40,7 +40,8 @@
 // logits and gradients are overwritten at the members after the dense pass.
 // Where a mask leaves few tokens they are visited one by one instead.
 //
-// The log-prob keeps one (max, sum) per row and segment.  Its dense part adds in
+// The log-prob keeps one (max, sum) per row and segment, folded by the CTA that has
+// the whole row or, where ranges share it, by a second launch.  Its dense part adds in
 // an order that depends on V and the type alone, its members' part adds integers,
 // so the bits do not depend on the columns or rows per CTA, the chain, the
 // strides or the other rows of the batch.
